@@ -91,6 +91,7 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_GROUP_MAX_N 4096   /* largest window for spec_group_same_length */
 #define SPEC_PROC_MAX_V 524288  /* largest vocabulary for the processed-distribution calls */
 #define SPEC_TREE_MAX_N 256     /* largest candidate tree (nodes per sequence) */
+#define SPEC_ATTN_MAX_D 256     /* largest head of the attention calls */
 
 /* Human-readable name of a return code. */
 const char *spec_strerror(int code);
@@ -539,6 +540,141 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
                            int32_t *perm, int32_t *batch_start, int32_t *batch_len,
                            int32_t *num_batches, int32_t *num_grouped,
                            spec_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * The attention half of the verify forward.
+ * [Walkthrough] 5.2 lists positions and a visibility mask among a tree
+ * verifier's fields; [Forensics] 3 and 3.1 tie every cached row to its
+ * position.  The pages leave the forward itself to the model; these calls are
+ * its part between the projections and the attention's output, on the caches
+ * that the commit calls keep: the left-padded rectangle [L][2][B][H][C][D]
+ * (sequence b's n_b rows at columns [E - n_b, E)), or, in the _paged forms, a
+ * pool of pages [L][2][pages][H][page_size][D], row r of sequence b at row
+ * r % page_size of page block_table[b, r / page_size].  A ragged pool
+ * [L][2][N][H][Cs][D] is a pool of N pages of Cs rows (max_pages = 1,
+ * block_table = the members' indices).
+ *
+ * Shared arguments
+ *   kv / pool    the cache, of dt (bf16 or f32); `layer` in [0, L) is used
+ *   G            query heads per KV head (>= 1); query head h * G + g reads KV
+ *                head h
+ *   D            head size: D * element size a multiple of 16, at most
+ *                SPEC_ATTN_MAX_D
+ *   q, q_stride  query rows [tokens][H * G][D] of dt, q_stride elements from
+ *                token to token (a view of a fused projection will do); so
+ *                k, k_stride and v, v_stride ([tokens][H][D])
+ *   All pointers to elements of dt and all strides are multiples of 16 bytes.
+ *   end_col      device scalar E; kv_len [B] int32 n_b
+ *   block_table  [B, max_pages] int32
+ *   status       [B] out or NULL: SPEC_ST_CAPACITY if the rows do not fit the
+ *                rectangle or the table; SPEC_ST_BAD_STATE for lengths out of
+ *                range and for a page id outside [0, pages) (never used as an
+ *                address).  Sequences with a nonzero status: their cache is
+ *                not written, except that rows on good pages may be; their
+ *                attention output is zero, or unspecified where a page id is
+ *                bad.  Other sequences are not affected.
+ * No call takes a gradient; bf16 results are float32 results rounded once.
+ * Sums, maxima and statistics are float32.
+ *
+ * spec_tree_mask -- positions and visibility of a tree's nodes, once per round
+ * for all layers.
+ *   first_child, next_sibling  [B, N] links as in spec_verify_tree
+ *   kv_len       [B] n_b
+ *   positions    [B, N] out: n_b + depth (the root's depth is 0); n_b for a
+ *                node that no path from the root reaches
+ *   mask         [B, N, ceil(N / 32)] out: bit j % 32 of word j / 32 of node i
+ *                is set iff j is on the path from the root to i (i included);
+ *                0 for a node that no path reaches
+ *   status       SPEC_ST_BAD_STATE for links that do not point forward inside
+ *                the tree, a node that two links reach (all of that tree's
+ *                masks are 0 then) or n_b < 0
+ * Errors: SPEC_EINVAL for NULL required pointers, sizes < 1, overlap;
+ * SPEC_ECAPACITY for N > SPEC_TREE_MAX_N.
+ *
+ * spec_norm_rope_kv -- norms queries and keys per head, rotates them by their
+ * positions, writes queries to q_out and keys and values into the cache.
+ *   y = x * w / sqrt(mean(x^2) + eps) over a head's D elements (q_weight,
+ *   k_weight [D] of dt, or NULL for no norm); then for pair i < rot / 2 with
+ *   t = position * inv_freq[i]:
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t), a = i,
+ *   b = i + rot / 2, or with interleaved != 0 a = 2i, b = 2i + 1.  Elements
+ *   from rot on are kept.  The result of the norm is not rounded in between.
+ *   T            tokens in all, packed in q, k and v
+ *   N, cu_seqlens  N >= 1 and NULL: T = B * N, the verify forward's slots: node
+ *                i of sequence b becomes row n_b + i (column E + i).  N = 0 and
+ *                [B + 1] int32: prompts; sequence b's tokens are
+ *                [cu_seqlens[b], cu_seqlens[b + 1]) and become its last rows, so
+ *                kv_len and E count them already.  Tokens of no sequence are
+ *                left alone.
+ *   positions    [T] int32 or NULL: each token's row number
+ *   inv_freq     [rot / 2] float32 (NULL if rot is 0); rot even, 0 .. D
+ *   q_out        [T, H * G, D] out, contiguous
+ *
+ * spec_prompt_attention -- causal attention of packed prompts whose rows are
+ * in the cache: token i of sequence b's len = cu_seqlens[b + 1] - cu_seqlens[b]
+ * sees rows [0, n_b - len + i]; kv_len and E count the prompt's rows.
+ *   out          [T, H * G, D] out, contiguous
+ *   lse          [T, H * G] float32 out or NULL: the log of the sum of
+ *                exp(scale * q.k) over the rows seen
+ *   scale        > 0
+ *
+ * spec_tree_attention -- attention of the N nodes of each sequence, whose
+ * slots the forward has written at rows n_b .. n_b + N - 1 (columns E ..
+ * E + N - 1): node i sees the n_b cached rows and the nodes that its mask row
+ * gives (mask as from spec_tree_mask, any bits allowed); with mask NULL (a
+ * linear draft; N = 1: one token) the nodes 0 .. i.  A node whose mask row is 0
+ * sees nothing at all.
+ *   q            [B, N, H * G, D] with one stride from token to token
+ *   out          [B, N, H * G, D] out; lse [B, N, H * G] out or NULL
+ *   ws           workspace of spec_tree_attention_workspace_bytes(B, N, H, G,
+ *                D, max_rows, dt), max_rows = C, or max_pages * page_size
+ *                (contents ignored on entry; NULL if the query is 0)
+ * A row that sees nothing, or only scores of -inf, gives zeros and an lse of
+ * -inf.  Rows that are not seen may hold anything, infinities and NaNs too.
+ * Results do not depend on the other sequences' values and are the same in
+ * every call.
+ * Errors of these calls: SPEC_EINVAL for NULL required pointers, sizes < 1,
+ * layer outside [0, L), strides or addresses that are not multiples of 16
+ * bytes, scale or eps out of range, outputs that overlap inputs or each other,
+ * counts of 2^31 and more; SPEC_ECAPACITY for D > SPEC_ATTN_MAX_D or
+ * N > SPEC_TREE_MAX_N; SPEC_EWORKSPACE.
+ * ------------------------------------------------------------------------ */
+int spec_tree_mask(int B, int N, const int32_t *first_child, const int32_t *next_sibling,
+                   const int32_t *kv_len, int32_t *positions, uint32_t *mask, int32_t *status,
+                   spec_stream_t stream);
+int spec_norm_rope_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, void *kv, spec_dtype dt, int L, int B, int H, int C, int D,
+                      int layer, int T, int N, int G, const int32_t *end_col, const int32_t *kv_len,
+                      const int32_t *cu_seqlens, const int32_t *positions, const void *q_weight,
+                      const void *k_weight, float eps, const float *inv_freq, int rot, int interleaved,
+                      void *q_out, int32_t *status, spec_stream_t stream);
+int spec_norm_rope_kv_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const void *v, int64_t v_stride, void *pool, spec_dtype dt, int L, int pages,
+                            int H, int page_size, int D, int layer, int T, int B, int N, int G,
+                            const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                            const int32_t *cu_seqlens, const int32_t *positions, const void *q_weight,
+                            const void *k_weight, float eps, const float *inv_freq, int rot,
+                            int interleaved, void *q_out, int32_t *status, spec_stream_t stream);
+int spec_prompt_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B,
+                          int H, int C, int D, int layer, int T, int G, const int32_t *end_col,
+                          const int32_t *kv_len, const int32_t *cu_seqlens, float scale, void *out,
+                          float *lse, int32_t *status, spec_stream_t stream);
+int spec_prompt_attention_paged(const void *q, int64_t q_stride, const void *pool, spec_dtype dt, int L,
+                                int pages, int H, int page_size, int D, int layer, int B, int T, int G,
+                                const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                                const int32_t *cu_seqlens, float scale, void *out, float *lse,
+                                int32_t *status, spec_stream_t stream);
+size_t spec_tree_attention_workspace_bytes(int B, int N, int H, int G, int D, int max_rows,
+                                           spec_dtype dt);
+int spec_tree_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B,
+                        int H, int C, int D, int layer, int N, int G, const int32_t *end_col,
+                        const int32_t *kv_len, const uint32_t *mask, float scale, void *out, float *lse,
+                        int32_t *status, void *ws, size_t ws_bytes, spec_stream_t stream);
+int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool, spec_dtype dt, int L,
+                              int pages, int H, int page_size, int D, int layer, int B, int N, int G,
+                              const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                              const uint32_t *mask, float scale, void *out, float *lse, int32_t *status,
+                              void *ws, size_t ws_bytes, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -44,3 +44,6 @@ from .tree_sample import tree_sample_verify  # noqa: F401
 from .unbatched import UnbatchedModel, check_ragged  # noqa: F401
 from .ragged import repad_kv, unpad_kv, ragged_bytes  # noqa: F401
 from .policy import eqspec_round, exspec_round  # noqa: F401
+from .attention import (  # noqa: F401
+    tree_paths, mask_words, norm_rope, row_places, cache_rows, attend,
+)

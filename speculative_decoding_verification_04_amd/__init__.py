@@ -17,7 +17,7 @@ SPEC_OK, SPEC_EINVAL, SPEC_EWORKSPACE, SPEC_ECAPACITY, SPEC_EHIP = 0, -1, -2, -3
 SPEC_ST_DRAFT_OOR, SPEC_ST_Q_ZERO, SPEC_ST_RESID_ZERO = 1, 2, 4
 SPEC_ST_NONFINITE, SPEC_ST_BAD_STATE, SPEC_ST_CAPACITY, SPEC_ST_INCOMPLETE = 8, 16, 32, 64
 SPEC_MAX_K, SPEC_GROUP_MAX_N, SPEC_PROC_MAX_V, SPEC_TREE_MAX_N = 127, 4096, 524288, 256
-SPEC_GREEDY_SCRATCH_BYTES = 8 << 20
+SPEC_GREEDY_SCRATCH_BYTES, SPEC_ATTN_MAX_D = 8 << 20, 256
 
 __all__ = [
     "SpecError", "spec_strerror", "spec_verify_greedy_workspace_bytes", "spec_verify_greedy",
@@ -27,6 +27,9 @@ __all__ = [
     "spec_commit_realign_kv", "spec_resync_draft_kv", "spec_repad_kv", "spec_unpad_kv", "spec_commit_paged",
     "spec_verify_tree_workspace_bytes", "spec_verify_tree", "spec_compact_tree_kv", "spec_verify_tree_sample_workspace_bytes",
     "spec_verify_tree_sample",
+    "spec_tree_mask", "spec_norm_rope_kv", "spec_norm_rope_kv_paged", "spec_prompt_attention",
+    "spec_prompt_attention_paged", "spec_tree_attention_workspace_bytes", "spec_tree_attention",
+    "spec_tree_attention_paged", "SPEC_ATTN_MAX_D",
     "spec_group_same_length", "workspace", "library",
 ]
 
@@ -356,3 +359,181 @@ def spec_group_same_length(lengths, B: int, min_group: int, perm, batch_start, b
         _arg(batch_len, "int32", N, "batch_len"), _arg(num_batches, "int32", 1, "num_batches"),
         _arg(num_grouped, "int32", 1, "num_grouped"), _stream(stream))
     _check(code, "spec_group_same_length")
+
+
+def spec_tree_mask(first_child, next_sibling, kv_len, positions, mask, *, status=None, stream=None) -> None:
+    """first_child, next_sibling [B, N], kv_len [B] int32; positions [B, N] int32 out, mask
+    [B, N, ceil(N / 32)] int32 out (bit words), for spec_norm_rope_kv and spec_tree_attention."""
+    B, N = first_child.shape
+    code = library().spec_tree_mask(
+        B, N, _arg(first_child, "int32", B * N, "first_child"), _arg(next_sibling, "int32", B * N, "next_sibling"),
+        _arg(kv_len, "int32", B, "kv_len"), _arg(positions, "int32", B * N, "positions"),
+        _arg(mask, "int32", B * N * ((N + 31) // 32), "mask"), _arg(status, "int32", B, "status", True),
+        _stream(stream))
+    _check(code, "spec_tree_mask")
+
+
+def _token_rows(t, heads: int, ref, name: str, tokens=None):
+    """Pointer and token stride (elements) of [..., heads, D] rows of ref's dtype and head size:
+    contiguous heads, one stride from token to token (a view of a fused projection will do)."""
+    if t.dtype != ref.dtype:
+        raise ValueError(f"{name} must be {ref.dtype}, not {t.dtype}")
+    D = ref.shape[-1]
+    if t.dim() not in (3, 4) or tuple(t.shape[-2:]) != (heads, D):
+        raise ValueError(f"{name} must be [..., {heads}, {D}], got {tuple(t.shape)}")
+    count = 1
+    for x in t.shape[:-2]:
+        count *= x
+    if tokens is not None and count != tokens:
+        raise ValueError(f"{name} needs {tokens} tokens, has {count}")
+    if not t.is_cuda:
+        raise ValueError("tensor must be on the GPU")
+    step = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else heads * D)
+    if (D > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != step * t.shape[1]:
+        raise ValueError(f"{name}: one stride from token to token is needed")
+    return ctypes.c_void_p(t.data_ptr()), int(step), count
+
+
+def _cache_dims(kv, heads: int, G_of: str):
+    """Sizes of a cache [L, 2, planes, H, cols, D] and the group size of `heads` query heads."""
+    if kv.dim() != 6 or kv.shape[1] != 2:
+        raise ValueError("the cache must be [L, 2, planes, H, cols, D]")
+    L, _, planes, H, cols, D = kv.shape
+    if heads < H or heads % H:
+        raise ValueError(f"{G_of} has {heads} heads, the cache {H}: no whole group")
+    return L, planes, H, cols, D, heads // H
+
+
+def _block_table(block_table):
+    B, max_pages = block_table.shape
+    return _arg(block_table, "int32", B * max_pages, "block_table"), B, max_pages
+
+
+def _norm_rope(name, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
+               inv_freq, interleaved, status, stream):
+    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
+    qp, qs, T = _token_rows(q, H * G, kv, "q")
+    kp, ks, _ = _token_rows(k, H, kv, "k", T)
+    vp, vs, _ = _token_rows(v, H, kv, "v", T)
+    if q_out.dtype != kv.dtype or q_out.numel() != T * H * G * D:
+        raise ValueError(f"q_out must hold {T} tokens of {H * G} x {D} {kv.dtype}")
+    dt = str(kv.dtype).replace("torch.", "")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    paged = name.endswith("_paged")
+    if paged:
+        table, B, max_pages = _block_table(where)
+        place = [table, max_pages]
+    else:
+        B, place = planes, [_arg(where, "int32", 1, "end_col")]
+    if cu_seqlens is None and (T % B or not T):
+        raise ValueError(f"{T} tokens are no whole number for each of {B} sequences")
+    N = T // B if cu_seqlens is None else 0
+    sizes = [planes, H, cols, D, int(layer), T] + ([B] if paged else []) + [N, G]
+    code = getattr(library(), name)(
+        qp, qs, kp, ks, vp, vs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
+        _arg(cu_seqlens, "int32", B + 1, "cu_seqlens", True), _arg(positions, "int32", T, "positions", True),
+        _arg(q_weight, dt, D, "q_weight", True), _arg(k_weight, dt, D, "k_weight", True), float(eps),
+        _arg(inv_freq, "float32", 0, "inv_freq", True) if rot else None, rot, int(bool(interleaved)), _ptr(q_out),
+        _arg(status, "int32", B, "status", True), _stream(stream))
+    _check(code, name)
+
+
+def spec_norm_rope_kv(q, k, v, kv, layer: int, end_col, kv_len, q_out, *, cu_seqlens=None, positions=None,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False,
+                      status=None, stream=None) -> None:
+    """q [..., H * G, D], k, v [..., H, D] (views of a fused projection will do), kv [L, 2, B, H, C, D]:
+    norms and rotates queries (to q_out) and keys, and writes keys and values into the cache slots.
+    Without cu_seqlens B sequences of N tokens at columns E .. E + N - 1; with it packed prompts."""
+    _norm_rope("spec_norm_rope_kv", q, k, v, kv, layer, end_col, kv_len, q_out, cu_seqlens, positions, q_weight,
+               k_weight, eps, inv_freq, interleaved, status, stream)
+
+
+def spec_norm_rope_kv_paged(q, k, v, pool, layer: int, block_table, kv_len, q_out, *, cu_seqlens=None,
+                            positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                            interleaved: bool = False, status=None, stream=None) -> None:
+    """spec_norm_rope_kv into a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages] int32."""
+    _norm_rope("spec_norm_rope_kv_paged", q, k, v, pool, layer, block_table, kv_len, q_out, cu_seqlens, positions,
+               q_weight, k_weight, eps, inv_freq, interleaved, status, stream)
+
+
+def _out_rows(out, q, name: str = "out"):
+    if out.dtype != q.dtype or out.numel() != q.numel():
+        raise ValueError(f"{name} must match {tuple(q.shape)} {q.dtype}, got {tuple(out.shape)} {out.dtype}")
+    return _ptr(out)
+
+
+def _scale(scale, D: int) -> float:
+    return float(D) ** -0.5 if scale is None else float(scale)
+
+
+def _prompt(name, q, kv, layer, cu_seqlens, where, kv_len, out, scale, lse, status, stream):
+    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
+    qp, qs, T = _token_rows(q, H * G, kv, "q")
+    if name.endswith("_paged"):
+        table, B, max_pages = _block_table(where)
+        sizes, place = [planes, H, cols, D, int(layer), B, T, G], [table, max_pages]
+    else:
+        B = planes
+        sizes, place = [B, H, cols, D, int(layer), T, G], [_arg(where, "int32", 1, "end_col")]
+    code = getattr(library(), name)(
+        qp, qs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
+        _arg(cu_seqlens, "int32", B + 1, "cu_seqlens"), _scale(scale, D), _out_rows(out, q),
+        _arg(lse, "float32", T * H * G, "lse", True), _arg(status, "int32", B, "status", True), _stream(stream))
+    _check(code, name)
+
+
+def spec_prompt_attention(q, kv, layer: int, cu_seqlens, end_col, kv_len, out, *, scale=None, lse=None, status=None,
+                          stream=None) -> None:
+    """Causal attention of packed prompts q [T, H * G, D] over the cache kv [L, 2, B, H, C, D] that holds
+    their rows; out [T, H * G, D].  scale: 1 / sqrt(D) if None."""
+    _prompt("spec_prompt_attention", q, kv, layer, cu_seqlens, end_col, kv_len, out, scale, lse, status, stream)
+
+
+def spec_prompt_attention_paged(q, pool, layer: int, cu_seqlens, block_table, kv_len, out, *, scale=None, lse=None,
+                                status=None, stream=None) -> None:
+    """spec_prompt_attention over a page pool [L, 2, pages, H, page_size, D]."""
+    _prompt("spec_prompt_attention_paged", q, pool, layer, cu_seqlens, block_table, kv_len, out, scale, lse, status,
+            stream)
+
+
+def spec_tree_attention_workspace_bytes(B: int, N: int, H: int, G: int, D: int, max_rows: int,
+                                        dtype_code: int) -> int:
+    """max_rows: C of the rectangle, or max_pages * page_size."""
+    return int(library().spec_tree_attention_workspace_bytes(B, N, H, G, D, max_rows, dtype_code))
+
+
+def _tree(name, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, status, stream):
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, heads, D], got {tuple(q.shape)}")
+    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
+    qp, qs, T = _token_rows(q, H * G, kv, "q")
+    B, N = q.shape[:2]
+    if name.endswith("_paged"):
+        table, rows, max_pages = _block_table(where)
+        sizes, place = [planes, H, cols, D, int(layer), B, N, G], [table, max_pages]
+    else:
+        rows, sizes, place = planes, [planes, H, cols, D, int(layer), N, G], [_arg(where, "int32", 1, "end_col")]
+    if rows != B:
+        raise ValueError(f"q has {B} sequences, the cache {rows}")
+    code = getattr(library(), name)(
+        qp, qs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
+        _arg(mask, "int32", B * N * ((N + 31) // 32), "mask", True), _scale(scale, D), _out_rows(out, q),
+        _arg(lse, "float32", T * H * G, "lse", True), _arg(status, "int32", B, "status", True),
+        None if ws is None else _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check(code, name)
+
+
+def spec_tree_attention(q, kv, layer: int, end_col, kv_len, out, ws=None, *, mask=None, scale=None, lse=None,
+                        status=None, stream=None) -> None:
+    """Attention of q [B, N, H * G, D] (the verify forward's nodes, their slots already at columns
+    E .. E + N - 1 of kv [L, 2, B, H, C, D]) over the cached rows and each node's visible nodes;
+    mask [B, N, ceil(N / 32)] int32 as from spec_tree_mask, None: a chain.  out [B, N, H * G, D]."""
+    _tree("spec_tree_attention", q, kv, layer, end_col, kv_len, out, ws, mask, scale, lse, status, stream)
+
+
+def spec_tree_attention_paged(q, pool, layer: int, block_table, kv_len, out, ws=None, *, mask=None, scale=None,
+                              lse=None, status=None, stream=None) -> None:
+    """spec_tree_attention over a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages]."""
+    _tree("spec_tree_attention_paged", q, pool, layer, block_table, kv_len, out, ws, mask, scale, lse, status, stream)

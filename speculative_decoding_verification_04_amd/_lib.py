@@ -10,6 +10,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_S = ctypes.c_int64   # strides
 
 # name -> (restype, argtypes), mirroring include/spec_verify.h
 PROTOTYPES = {
@@ -41,6 +42,19 @@ PROTOTYPES = {
     "spec_verify_tree_sample_workspace_bytes": (_SZ, [_I, _I, _I]),
     "spec_verify_tree_sample": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, ctypes.c_int32, _P, _P, _P, _P,
                                      _P, _P, _P, _P, _P, _SZ, _P]),
+    "spec_tree_mask": (_I, [_I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "spec_norm_rope_kv": (_I, [_P, _S, _P, _S, _P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                               _P, _P, _F, _P, _I, _I, _P, _P, _P]),
+    "spec_norm_rope_kv_paged": (_I, [_P, _S, _P, _S, _P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I,
+                                     _P, _P, _P, _P, _P, _F, _P, _I, _I, _P, _P, _P]),
+    "spec_prompt_attention": (_I, [_P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _P, _P]),
+    "spec_prompt_attention_paged": (_I, [_P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _F, _P,
+                                         _P, _P, _P]),
+    "spec_tree_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "spec_tree_attention": (_I, [_P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _P, _P, _SZ,
+                                 _P]),
+    "spec_tree_attention_paged": (_I, [_P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _F, _P,
+                                       _P, _P, _P, _SZ, _P]),
     "spec_group_same_length": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 

@@ -1,0 +1,330 @@
+// Per-head norms of queries and keys, the position rotation, and the write of
+// K and V into the cache, in one pass (gfx950).
+//
+// For a head x of D elements at position p:
+//   y = x * w / sqrt(mean(x^2) + eps)            (w given; else y = x)
+//   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+//   t = p * inv_freq[i], pair i: (i, i + rot/2), or (2i, 2i + 1); the elements
+//   from rot on are not rotated.
+// V is copied.  Everything between the load and the one rounding at the store
+// is float32; the norm's result is not rounded before the rotation.  The angle
+// is reduced in float64 (p * inv_freq / 2 pi minus its nearest whole number),
+// since in float32 a position of 10^5 would leave 2^-7 of a radian.
+//
+// Design.  Bound by HBM: each element is read once and written once.  One
+// workgroup per token; a group of lanes takes one head, 16 bytes a lane, and
+// keeps its cosines and sines in registers over the heads that it takes, so a
+// token's angles are computed once for all its heads.  A lane reads its
+// partners' chunk itself (a second load of the same head, from the cache)
+// rather than exchanging eight values with another lane.
+#include "cache_view.h"
+
+namespace specv {
+namespace {
+
+constexpr int kMaxThreads = 256;
+
+struct RopeParams {
+  CacheView c;
+  const char *q, *k, *v;
+  long long q_stride, k_stride, v_stride;   // bytes from token to token
+  char *q_out;
+  int T, B, N, Hq, half, interleaved, lanes;  // N 0: packed; lanes: per head
+  const int32_t *cu, *positions;
+  const void *q_weight, *k_weight;
+  float eps;
+  const float *inv_freq;
+  int32_t *status;
+};
+
+template <typename T> struct Vec;
+template <> struct Vec<float> { static constexpr int n = 4; };
+template <> struct Vec<__bf16> { static constexpr int n = 8; };
+
+template <typename T>
+__device__ inline void load_chunk(const void *p, float (&x)[Vec<T>::n]) {
+  typedef T V __attribute__((ext_vector_type(Vec<T>::n)));
+  const V v = *static_cast<const V *>(p);
+#pragma unroll
+  for (int j = 0; j < Vec<T>::n; ++j) x[j] = static_cast<float>(v[j]);
+}
+
+template <typename T>
+__device__ inline void store_chunk(void *p, const float (&x)[Vec<T>::n]) {
+  typedef T V __attribute__((ext_vector_type(Vec<T>::n)));
+  V v;
+#pragma unroll
+  for (int j = 0; j < Vec<T>::n; ++j) v[j] = static_cast<T>(x[j]);
+  *static_cast<V *>(p) = v;
+}
+
+// A sequence's new tokens and where their rows start.
+struct Span {
+  int t0, len, row0;   // first token, tokens, first row
+  int st;              // status bits; nonzero: nothing is written to the cache
+};
+
+__device__ inline Span span_of(const RopeParams &P, int b) {
+  Span s;
+  const int n = P.c.kv_len[b];
+  s.st = 0;
+  if (P.cu) {
+    s.t0 = P.cu[b];
+    s.len = P.cu[b + 1] - s.t0;
+    if (s.t0 < 0 || s.len < 0 || P.cu[b + 1] > P.T) s.st = SPEC_ST_BAD_STATE;
+    s.row0 = n - s.len;
+    if (s.row0 < 0) s.st |= SPEC_ST_BAD_STATE;
+  } else {
+    s.t0 = b * P.N;
+    s.len = P.N;
+    s.row0 = n;
+    if (n < 0) s.st = SPEC_ST_BAD_STATE;
+  }
+  const long long cap = cache_capacity(P.c);
+  if (P.c.table) {
+    if (static_cast<long long>(s.row0) + s.len > cap) s.st |= SPEC_ST_CAPACITY;
+  } else {
+    const int E = *P.c.end_col;
+    if (E < 0 || static_cast<long long>(E) + (P.cu ? 0 : P.N) > cap) s.st |= SPEC_ST_CAPACITY;
+    if (n > E) s.st |= SPEC_ST_BAD_STATE;
+  }
+  return s;
+}
+
+// The status of one sequence per wave: its span and the pages of its new rows.
+__device__ inline void write_status(const RopeParams &P, int b) {
+  const int lane = threadIdx.x & (kWave - 1);
+  if (b >= P.B) return;
+  const Span s = span_of(P, b);
+  int st = s.st;
+  if (!st && P.c.table && s.len > 0) {
+    bool bad = false;
+    const int last = cache_page(P.c, s.row0 + s.len - 1);
+    for (int i = cache_page(P.c, s.row0) + lane; i <= last; i += kWave) {
+      const int page = P.c.table[static_cast<long long>(b) * P.c.max_pages + i];
+      bad |= page < 0 || page >= P.c.planes;
+    }
+    if (__any(bad)) st = SPEC_ST_BAD_STATE;
+  }
+  if (lane == 0) P.status[b] = st;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kMaxThreads) void norm_rope_kernel(RopeParams P) {
+  constexpr int kN = Vec<T>::n;
+  const int lane = threadIdx.x & (kWave - 1);
+  if (blockIdx.x >= static_cast<unsigned>(P.T)) {
+    write_status(P, (blockIdx.x - P.T) * (blockDim.x / kWave) + threadIdx.x / kWave);
+    return;
+  }
+  const int t = blockIdx.x;
+  int b = -1;
+  if (P.cu) {
+    // the first sequence that holds token t
+    for (int b0 = 0; b0 < P.B; b0 += kWave) {
+      const int i = b0 + lane;
+      const bool holds = i < P.B && P.cu[i] <= t && t < P.cu[i + 1];
+      const uint64_t who = __ballot(holds);
+      if (who) {
+        b = b0 + __ffsll(static_cast<unsigned long long>(who)) - 1;
+        break;
+      }
+    }
+    if (b < 0) return;                                    // behind the last sequence
+  } else {
+    b = t / P.N;
+  }
+  const Span s = span_of(P, b);
+  const int row = s.row0 + (t - s.t0);
+  bool write = s.st == 0;
+  long long slot = 0;                                     // K's and V's offset of head 0
+  if (write) {
+    int plane = b, col = row;
+    if (P.c.table) {
+      const int i = cache_page(P.c, row);
+      plane = P.c.table[static_cast<long long>(b) * P.c.max_pages + i];
+      col = row - i * P.c.cols;
+      write = plane >= 0 && plane < P.c.planes;
+    } else {
+      col = *P.c.end_col - P.c.kv_len[b] + row;
+    }
+    slot = cache_offset(P.c, write ? plane : 0, 0, col, sizeof(T));
+  }
+  const long long head_step = static_cast<long long>(P.c.cols) * P.c.D * sizeof(T);
+  const int D = P.c.D, half = P.half;
+  const int lph = P.lanes, g = threadIdx.x / lph, e0 = (threadIdx.x & (lph - 1)) * kN;
+  const bool active = e0 < D;
+  const int pos = P.positions ? P.positions[t] : row;
+  // This lane's angles and partners: element e's partner is e ^ 1, or
+  // e + half, or e - half; c = cos, sn = sin with the sign that its side takes.
+  float c[kN], sn[kN];
+  int mate[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    const int e = e0 + j;
+    c[j] = 1.0f;
+    sn[j] = 0.0f;
+    mate[j] = min(e, D - 1);
+    if (active && e < 2 * half) {
+      const int i = P.interleaved ? e >> 1 : (e < half ? e : e - half);
+      const bool low = P.interleaved ? !(e & 1) : e < half;
+      const double turn = static_cast<double>(pos) * P.inv_freq[i] * 0.15915494309189533577;
+      float sv, cv;
+      sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sv, &cv);
+      c[j] = cv;
+      sn[j] = low ? -sv : sv;
+      mate[j] = P.interleaved ? e ^ 1 : (low ? e + half : e - half);
+    }
+  }
+  const bool whole = half % kN == 0;                      // a chunk's partners are one chunk
+  const int heads = P.Hq + 2 * P.c.H, step = blockDim.x / lph;
+  for (int h = g; h < heads; h += step) {
+    const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.c.H;
+    const int hh = is_q ? h : is_k ? h - P.Hq : h - P.Hq - P.c.H;
+    const char *src = (is_q ? P.q + t * P.q_stride : is_k ? P.k + t * P.k_stride : P.v + t * P.v_stride) +
+                      static_cast<long long>(hh) * D * sizeof(T);
+    float x[kN] = {};
+    if (active) load_chunk<T>(src + e0 * sizeof(T), x);
+    if (is_q || is_k) {
+      const void *wp = is_q ? P.q_weight : P.k_weight;
+      float y[kN] = {};
+      if (active) {
+        if (P.interleaved) {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) y[j] = x[j ^ 1];
+        } else if (whole) {
+          if (mate[0] != e0) load_chunk<T>(src + mate[0] * sizeof(T), y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) y[j] = static_cast<float>(reinterpret_cast<const T *>(src)[mate[j]]);
+        }
+      }
+      if (wp) {                                           // uniform over the lanes of a head
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) ss = fmaf(x[j], x[j], ss);
+        for (int d = lph >> 1; d; d >>= 1) ss += __shfl_xor(ss, d);
+        const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + P.eps);
+        const T *w = static_cast<const T *>(wp);
+        if (active) {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            x[j] = x[j] * r * static_cast<float>(w[e0 + j]);
+            y[j] = y[j] * r * static_cast<float>(w[mate[j]]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kN; ++j) x[j] = e0 + j < 2 * half ? fmaf(y[j], sn[j], x[j] * c[j]) : x[j];
+    }
+    if (active) {
+      if (is_q)
+        store_chunk<T>(P.q_out + (static_cast<long long>(t) * P.Hq + hh) * D * sizeof(T) + e0 * sizeof(T), x);
+      else if (write)
+        store_chunk<T>((is_k ? P.c.k : P.c.v) + slot + hh * head_step + e0 * sizeof(T), x);
+    }
+  }
+}
+
+int norm_rope_call(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, void *kv, spec_dtype dt, int L, int planes, int H, int cols, int D, int layer,
+                   int T, int B, int N, int G, const int32_t *table, int max_pages, bool paged,
+                   const int32_t *end_col, const int32_t *kv_len, const int32_t *cu, const int32_t *positions,
+                   const void *q_weight, const void *k_weight, float eps, const float *inv_freq, int rot,
+                   int interleaved, void *q_out, int32_t *status, spec_stream_t stream) {
+  if (!q || !k || !v || !q_out || (rot && !inv_freq)) return SPEC_EINVAL;
+  RopeParams P;
+  const int err = cache_view(P.c, kv, dt, L, planes, H, cols, D, layer, table, max_pages, paged, end_col, kv_len);
+  if (err) return err;
+  if (T < 1 || B < 1 || G < 1 || (!paged && planes != B)) return SPEC_EINVAL;
+  if (cu ? N != 0 : N < 1 || static_cast<long long>(B) * N != T) return SPEC_EINVAL;
+  if (rot < 0 || rot > D || rot % 2 || !(eps >= 0.0f) || eps > 3.4e38f) return SPEC_EINVAL;
+  if (D > SPEC_ATTN_MAX_D) return SPEC_ECAPACITY;
+  const int elt = dt == SPEC_BF16 ? 2 : 4, Hq = H * G;
+  if (static_cast<long long>(H) * (G + 2) >= INT32_MAX / D || static_cast<long long>(T) + B >= INT32_MAX)
+    return SPEC_EINVAL;
+  const long long qh = static_cast<long long>(Hq) * D, kh = static_cast<long long>(H) * D;
+  if (D * elt % 16 || q_stride < qh || k_stride < kh || v_stride < kh) return SPEC_EINVAL;
+  if (q_stride * elt % 16 || k_stride * elt % 16 || v_stride * elt % 16) return SPEC_EINVAL;
+  const void *wide[] = {q, k, v, kv, q_out};
+  for (const void *p : wide)
+    if (!aligned(p, 16)) return SPEC_EINVAL;
+  if (!aligned(q_weight, elt) || !aligned(k_weight, elt) || !aligned(inv_freq, 4)) return SPEC_EINVAL;
+  const size_t b4 = static_cast<size_t>(B) * 4, d = static_cast<size_t>(D) * elt;
+  const void *ins[] = {q, k, v, table, end_col, kv_len, cu, positions, q_weight, k_weight, inv_freq};
+  const size_t in_n[] = {((T - 1) * static_cast<size_t>(q_stride) + qh) * elt,
+                         ((T - 1) * static_cast<size_t>(k_stride) + kh) * elt,
+                         ((T - 1) * static_cast<size_t>(v_stride) + kh) * elt,
+                         paged ? b4 * max_pages : 0, paged ? 0u : 4u, b4, b4 + 4, static_cast<size_t>(T) * 4, d, d,
+                         static_cast<size_t>(rot) * 2};
+  const void *outs[] = {kv, q_out, status};
+  const size_t out_n[] = {cache_bytes(dt, L, planes, H, cols, D), static_cast<size_t>(T) * qh * elt, b4};
+  for (int o = 0; o < 3; ++o) {
+    for (int j = 0; j < 11; ++j)
+      if (overlaps(outs[o], out_n[o], ins[j], in_n[j])) return SPEC_EINVAL;
+    for (int j = o + 1; j < 3; ++j)
+      if (overlaps(outs[o], out_n[o], outs[j], out_n[j])) return SPEC_EINVAL;
+  }
+  P.q = static_cast<const char *>(q);
+  P.k = static_cast<const char *>(k);
+  P.v = static_cast<const char *>(v);
+  P.q_stride = q_stride * elt;
+  P.k_stride = k_stride * elt;
+  P.v_stride = v_stride * elt;
+  P.q_out = static_cast<char *>(q_out);
+  P.T = T;
+  P.B = B;
+  P.N = N;
+  P.Hq = Hq;
+  P.half = rot / 2;
+  P.interleaved = interleaved != 0;
+  P.lanes = 1;
+  while (P.lanes * (16 / elt) < D) P.lanes *= 2;
+  P.cu = cu;
+  P.positions = positions;
+  P.q_weight = q_weight;
+  P.k_weight = k_weight;
+  P.eps = eps;
+  P.inv_freq = inv_freq;
+  P.status = status;
+  // one token's heads, in whole waves
+  const long long lanes = static_cast<long long>(H) * (G + 2) * P.lanes;
+  const int threads = static_cast<int>(lanes < kMaxThreads ? round_up(lanes, kWave) : kMaxThreads);
+  const int waves = threads / kWave;
+  const unsigned grid = static_cast<unsigned>(T) + (status ? (B + waves - 1) / waves : 0);
+  (void)hipGetLastError();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dt == SPEC_BF16)
+    hipLaunchKernelGGL(norm_rope_kernel<__bf16>, dim3(grid), dim3(threads), 0, s, P);
+  else
+    hipLaunchKernelGGL(norm_rope_kernel<float>, dim3(grid), dim3(threads), 0, s, P);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace specv
+
+using namespace specv;
+
+extern "C" int spec_norm_rope_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, void *kv, spec_dtype dt, int L, int B, int H, int C, int D,
+                                 int layer, int T, int N, int G, const int32_t *end_col, const int32_t *kv_len,
+                                 const int32_t *cu_seqlens, const int32_t *positions, const void *q_weight,
+                                 const void *k_weight, float eps, const float *inv_freq, int rot, int interleaved,
+                                 void *q_out, int32_t *status, spec_stream_t stream) {
+  return norm_rope_call(q, q_stride, k, k_stride, v, v_stride, kv, dt, L, B, H, C, D, layer, T, B, N, G, nullptr, 0,
+                        false, end_col, kv_len, cu_seqlens, positions, q_weight, k_weight, eps, inv_freq, rot,
+                        interleaved, q_out, status, stream);
+}
+
+extern "C" int spec_norm_rope_kv_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                       const void *v, int64_t v_stride, void *pool, spec_dtype dt, int L, int pages,
+                                       int H, int page_size, int D, int layer, int T, int B, int N, int G,
+                                       const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                                       const int32_t *cu_seqlens, const int32_t *positions, const void *q_weight,
+                                       const void *k_weight, float eps, const float *inv_freq, int rot,
+                                       int interleaved, void *q_out, int32_t *status, spec_stream_t stream) {
+  return norm_rope_call(q, q_stride, k, k_stride, v, v_stride, pool, dt, L, pages, H, page_size, D, layer, T, B, N,
+                        G, block_table, max_pages, true, nullptr, kv_len, cu_seqlens, positions, q_weight, k_weight,
+                        eps, inv_freq, rot, interleaved, q_out, status, stream);
+}

@@ -1,0 +1,171 @@
+// Causal attention of packed prompts over the cache (gfx950).
+//
+// The tokens of B sequences lie packed; sequence b's are tokens
+// [cu[b], cu[b + 1]) and the last cu[b + 1] - cu[b] of its n_b cached rows are
+// theirs (so a prompt may follow rows that are cached already).  Token i of
+// len sees rows [0, n_b - len + i].
+//
+// Design.  Bound by the matrix cores: 4 D flops a visible pair against the
+// 2 D bytes of a row, which a tile of 128 query rows uses 128 times.  The
+// lengths are on the device, so the grid is the largest that T tokens in B
+// sequences can need, and a workgroup finds its (sequence, tile) by a scan over
+// the sequences' tile counts.  A sequence's tiles run from its last, the
+// longest walk, to its first.
+#include "attention.h"
+
+namespace specv {
+namespace {
+using namespace attn;
+
+constexpr int kRW = 4;
+constexpr int kTileRows = 32 * kRW;
+
+struct Where {
+  int b, tile, tiles;
+};
+
+// State of sequence b: its tokens (-1: they are not inside [0, T)) and status.
+__device__ inline int prompt_len(const Params &P, int b) {
+  const int lo = P.cu[b], hi = P.cu[b + 1];
+  return lo >= 0 && lo <= hi && hi <= P.T ? hi - lo : -1;
+}
+__device__ inline int prompt_status(const Params &P, int b, int len) {
+  if (len < 0) return SPEC_ST_BAD_STATE;
+  const int n = P.c.kv_len[b];
+  int st = n < len ? SPEC_ST_BAD_STATE : 0;
+  const long long cap = cache_capacity(P.c);
+  if (P.c.table) {
+    if (n > cap) st |= SPEC_ST_CAPACITY;
+  } else {
+    const int E = *P.c.end_col;
+    if (E < 0 || E > cap) st |= SPEC_ST_CAPACITY;
+    if (n > E) st |= SPEC_ST_BAD_STATE;
+  }
+  return st;
+}
+
+// The sequence and tile of flat tile number f; b = -1 past the last.
+__device__ inline Where find_tile(const Params &P, int f) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int base = 0;
+  for (int b0 = 0; b0 < P.B; b0 += kWave) {
+    const int b = b0 + lane;
+    const int len = b < P.B ? prompt_len(P, b) : 0;
+    const int tiles = len > 0 ? static_cast<int>((static_cast<long long>(len) * P.G + kTileRows - 1) / kTileRows) : 0;
+    const int upto = wave_incl_scan(tiles);
+    const uint64_t who = __ballot(base + upto > f);
+    if (who) {
+      const int l = __ffsll(static_cast<unsigned long long>(who)) - 1;
+      const int n = read_lane(tiles, l);
+      const int before = base + read_lane(upto, l) - n;
+      return Where{b0 + l, n - 1 - (f - before), n};
+    }
+    base += read_lane(upto, kWave - 1);
+  }
+  return Where{-1, 0, 0};
+}
+
+template <typename T, int DP, bool PAGED>
+__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void prompt_kernel(Params P) {
+  using S = Shape<T, DP, kRW>;
+  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  const int H = P.c.H;
+  const int h = blockIdx.x % H, f = blockIdx.x / H;
+  if (blockIdx.x == 0 && P.status) {
+    // sequences without tokens have no tile that would report on them
+    for (int b = threadIdx.x; b < P.B; b += kThreads) {
+      const int len = prompt_len(P, b);
+      if (len <= 0) P.status[b] = prompt_status(P, b, len);
+    }
+  }
+  const Where w = find_tile(P, f);
+  if (w.b < 0) return;
+  Job J;
+  const int len = prompt_len(P, w.b), st = prompt_status(P, w.b, len), n = P.c.kv_len[w.b];
+  J.b = w.b;
+  J.h = h;
+  J.row0 = w.tile * kTileRows;
+  J.tokens = len;
+  J.token0 = P.cu[w.b];
+  J.limit0 = n - len + 1;
+  J.total = n;
+  const bool reports = P.status && h == 0 && w.tile == w.tiles - 1;   // the tile that walks every row
+  if (st) {
+    put_zeros<T>(P, J, kTileRows);
+    if (reports && threadIdx.x == 0) P.status[w.b] = st;
+    return;
+  }
+  J.start_col = PAGED ? 0 : *P.c.end_col - n;
+  const int last = min((J.row0 + kTileRows - 1) / P.G, len - 1);      // the tile's last token
+  J.t0 = 0;
+  J.t1 = (J.limit0 + last + S::kKT - 1) / S::kKT;
+  const int bad = walk<T, DP, kRW, PAGED, true>(P, J, -1, lds);
+  if (reports && threadIdx.x == 0) P.status[w.b] = bad;
+}
+
+template <typename T, int DP>
+int launch_prompt(const Params &P, unsigned grid, hipStream_t s) {
+  if (P.c.table)
+    hipLaunchKernelGGL((prompt_kernel<T, DP, true>), dim3(grid), dim3(kThreads), 0, s, P);
+  else
+    hipLaunchKernelGGL((prompt_kernel<T, DP, false>), dim3(grid), dim3(kThreads), 0, s, P);
+  return launch_status();
+}
+
+int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int planes, int B, int H,
+                int cols, int D, int layer, int T, int G, const int32_t *table, int max_pages, bool paged,
+                const int32_t *end_col, const int32_t *kv_len, const int32_t *cu, float scale, void *out, float *lse,
+                int32_t *status, spec_stream_t stream) {
+  if (!cu) return SPEC_EINVAL;
+  Params P;
+  const int err = fill(P, q, q_stride, kv, dt, L, planes, B, H, cols, D, layer, G, table, max_pages, paged, end_col,
+                       kv_len, scale, out, lse, status);
+  if (err) return err;
+  if (T < 1) return SPEC_EINVAL;
+  const long long tiles = (static_cast<long long>(T) * G) / kTileRows + B;   // each sequence rounds up once
+  if (static_cast<long long>(T) * G >= INT32_MAX || tiles * H >= INT32_MAX) return SPEC_EINVAL;
+  const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
+  const void *ins[] = {q, kv, table, end_col, kv_len, cu};
+  const size_t in_n[] = {((T - 1) * static_cast<size_t>(q_stride) + hd) * elt, cache_bytes(dt, L, planes, H, cols, D),
+                         paged ? b4 * max_pages : 0, paged ? 0u : 4u, b4, b4 + 4};
+  const void *outs[] = {out, lse, status};
+  const size_t out_n[] = {T * hd * elt, static_cast<size_t>(T) * H * G * 4, b4};
+  for (int o = 0; o < 3; ++o) {
+    for (int j = 0; j < 6; ++j)
+      if (overlaps(outs[o], out_n[o], ins[j], in_n[j])) return SPEC_EINVAL;
+    for (int j = o + 1; j < 3; ++j)
+      if (overlaps(outs[o], out_n[o], outs[j], out_n[j])) return SPEC_EINVAL;
+  }
+  P.T = T;
+  P.cu = cu;
+  const unsigned grid = static_cast<unsigned>(tiles * H);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (dt == SPEC_BF16)
+    return D <= 64 ? launch_prompt<__bf16, 64>(P, grid, s)
+                   : D <= 128 ? launch_prompt<__bf16, 128>(P, grid, s) : launch_prompt<__bf16, 256>(P, grid, s);
+  return D <= 64 ? launch_prompt<float, 64>(P, grid, s)
+                 : D <= 128 ? launch_prompt<float, 128>(P, grid, s) : launch_prompt<float, 256>(P, grid, s);
+}
+
+}  // namespace
+}  // namespace specv
+
+using namespace specv;
+
+extern "C" int spec_prompt_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B,
+                                     int H, int C, int D, int layer, int T, int G, const int32_t *end_col,
+                                     const int32_t *kv_len, const int32_t *cu_seqlens, float scale, void *out,
+                                     float *lse, int32_t *status, spec_stream_t stream) {
+  return prompt_call(q, q_stride, kv, dt, L, B, B, H, C, D, layer, T, G, nullptr, 0, false, end_col, kv_len,
+                     cu_seqlens, scale, out, lse, status, stream);
+}
+
+extern "C" int spec_prompt_attention_paged(const void *q, int64_t q_stride, const void *pool, spec_dtype dt, int L,
+                                           int pages, int H, int page_size, int D, int layer, int B, int T, int G,
+                                           const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                                           const int32_t *cu_seqlens, float scale, void *out, float *lse,
+                                           int32_t *status, spec_stream_t stream) {
+  return prompt_call(q, q_stride, pool, dt, L, pages, B, H, page_size, D, layer, T, G, block_table, max_pages, true,
+                     nullptr, kv_len, cu_seqlens, scale, out, lse, status, stream);
+}

@@ -1,0 +1,151 @@
+"""Refusals of the attention calls: argument errors come back before any HIP
+call, and the binding checks what the C library cannot (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import speculative_decoding_verification_04_amd as sv
+
+try:
+    LIB = sv.library()
+except RuntimeError:
+    LIB = None
+
+needs_lib = pytest.mark.skipif(LIB is None, reason="libspecverify.so not built")
+
+# fake, never-dereferenced device addresses: validation fails before any use
+P = [ctypes.c_void_p(0x10000000 * (i + 1)) for i in range(14)]
+N = None
+ODD = ctypes.c_void_p(0x10000008)
+
+
+def _args(base, **kw):
+    a = dict(base)
+    for k in kw:
+        assert k in a, k
+    a.update(kw)
+    return tuple(a.values())
+
+
+MASK = dict(B=2, N=8, fc=P[0], ns=P[1], n=P[2], pos=P[3], mask=P[4], st=N, stream=N)
+ROPE = dict(q=P[0], qs=256, k=P[1], ks=128, v=P[2], vs=128, kv=P[3], dt=1, L=1, B=2, H=2, C=64, D=64, layer=0, T=6,
+            N=3, G=2, E=P[4], n=P[5], cu=N, pos=N, qw=N, kw=N, eps=1e-6, f=P[6], rot=64, near=0, out=P[7], st=N, s=N)
+ROPE_P = dict(q=P[0], qs=256, k=P[1], ks=128, v=P[2], vs=128, kv=P[3], dt=1, L=1, pages=5, H=2, page=16, D=64, layer=0,
+              T=6, B=2, N=3, G=2, table=P[4], most=4, n=P[5], cu=N, pos=N, qw=N, kw=N, eps=1e-6, f=P[6], rot=64, near=0,
+              out=P[7], st=N, s=N)
+PROMPT = dict(q=P[0], qs=256, kv=P[1], dt=1, L=2, B=2, H=2, C=64, D=64, layer=1, T=50, G=2, E=P[2], n=P[3], cu=P[4],
+              scale=0.125, out=P[5], lse=N, st=N, s=N)
+PROMPT_P = dict(q=P[0], qs=256, kv=P[1], dt=1, L=2, pages=9, H=2, page=16, D=64, layer=1, B=2, T=50, G=2, table=P[2],
+                most=4, n=P[3], cu=P[4], scale=0.125, out=P[5], lse=N, st=N, s=N)
+TREE = dict(q=P[0], qs=256, kv=P[1], dt=1, L=2, B=2, H=2, C=4096, D=64, layer=1, N=5, G=2, E=P[2], n=P[3], mask=N,
+            scale=0.125, out=P[4], lse=N, st=N, ws=P[5], wsb=1 << 27, s=N)
+TREE_P = dict(q=P[0], qs=256, kv=P[1], dt=1, L=2, pages=900, H=2, page=16, D=64, layer=1, B=2, N=5, G=2, table=P[2],
+              most=256, n=P[3], mask=N, scale=0.125, out=P[4], lse=N, st=N, ws=P[5], wsb=1 << 27, s=N)
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", [
+    (dict(fc=N), sv.SPEC_EINVAL), (dict(ns=N), sv.SPEC_EINVAL), (dict(n=N), sv.SPEC_EINVAL),
+    (dict(pos=N), sv.SPEC_EINVAL), (dict(mask=N), sv.SPEC_EINVAL), (dict(B=0), sv.SPEC_EINVAL),
+    (dict(N=0), sv.SPEC_EINVAL), (dict(N=257), sv.SPEC_ECAPACITY), (dict(pos=P[0]), sv.SPEC_EINVAL),
+    (dict(mask=P[3]), sv.SPEC_EINVAL), (dict(st=P[2]), sv.SPEC_EINVAL)])
+def test_tree_mask_refusals(kw, code):
+    assert LIB.spec_tree_mask(*_args(MASK, **kw)) == code
+
+
+COMMON = [(dict(q=N), sv.SPEC_EINVAL), (dict(kv=N), sv.SPEC_EINVAL), (dict(n=N), sv.SPEC_EINVAL),
+          (dict(out=N), sv.SPEC_EINVAL), (dict(dt=2), sv.SPEC_EINVAL), (dict(L=0), sv.SPEC_EINVAL),
+          (dict(B=0), sv.SPEC_EINVAL), (dict(H=0), sv.SPEC_EINVAL), (dict(D=0), sv.SPEC_EINVAL),
+          (dict(G=0), sv.SPEC_EINVAL), (dict(layer=-1), sv.SPEC_EINVAL), (dict(layer=2), sv.SPEC_EINVAL),
+          (dict(D=60), sv.SPEC_EINVAL), (dict(D=264, qs=2112), sv.SPEC_ECAPACITY), (dict(qs=248), sv.SPEC_EINVAL),
+          (dict(qs=257), sv.SPEC_EINVAL), (dict(q=ODD), sv.SPEC_EINVAL), (dict(kv=ODD), sv.SPEC_EINVAL),
+          (dict(out=ODD), sv.SPEC_EINVAL), (dict(out=P[0]), sv.SPEC_EINVAL), (dict(out=P[1]), sv.SPEC_EINVAL),
+          (dict(st=P[3]), sv.SPEC_EINVAL)]
+SCALES = [(dict(scale=x), sv.SPEC_EINVAL) for x in (0.0, -1.0, float("nan"), float("inf"))]
+PAGES = [(dict(table=N), sv.SPEC_EINVAL), (dict(pages=0), sv.SPEC_EINVAL), (dict(page=0), sv.SPEC_EINVAL),
+         (dict(most=0), sv.SPEC_EINVAL), (dict(most=1 << 28), sv.SPEC_EINVAL)]
+RECT = [(dict(E=N), sv.SPEC_EINVAL), (dict(C=0), sv.SPEC_EINVAL)]
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", COMMON + SCALES + RECT + [(dict(cu=N), sv.SPEC_EINVAL), (dict(T=0), sv.SPEC_EINVAL),
+                                                              (dict(T=1 << 30), sv.SPEC_EINVAL)])
+def test_prompt_refusals(kw, code):
+    assert LIB.spec_prompt_attention(*_args(PROMPT, **kw)) == code
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", COMMON + SCALES + PAGES + [(dict(cu=N), sv.SPEC_EINVAL), (dict(T=0), sv.SPEC_EINVAL)])
+def test_prompt_paged_refusals(kw, code):
+    assert LIB.spec_prompt_attention_paged(*_args(PROMPT_P, **kw)) == code
+
+
+TREES = [(dict(N=0), sv.SPEC_EINVAL), (dict(N=257), sv.SPEC_ECAPACITY), (dict(ws=N), sv.SPEC_EWORKSPACE),
+         (dict(wsb=1024), sv.SPEC_EWORKSPACE), (dict(ws=ctypes.c_void_p(0x60000010)), sv.SPEC_EWORKSPACE),
+         (dict(ws=P[1]), sv.SPEC_EINVAL), (dict(mask=ctypes.c_void_p(0x70000002)), sv.SPEC_EINVAL),
+         (dict(mask=P[4]), sv.SPEC_EINVAL)]
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", COMMON + SCALES + RECT + TREES)
+def test_tree_refusals(kw, code):
+    assert LIB.spec_tree_attention(*_args(TREE, **kw)) == code
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", COMMON + SCALES + PAGES + TREES)
+def test_tree_paged_refusals(kw, code):
+    assert LIB.spec_tree_attention_paged(*_args(TREE_P, **kw)) == code
+
+
+ROPES = [(dict(q=N), sv.SPEC_EINVAL), (dict(k=N), sv.SPEC_EINVAL), (dict(v=N), sv.SPEC_EINVAL),
+         (dict(kv=N), sv.SPEC_EINVAL), (dict(out=N), sv.SPEC_EINVAL), (dict(n=N), sv.SPEC_EINVAL),
+         (dict(f=N), sv.SPEC_EINVAL), (dict(T=0), sv.SPEC_EINVAL), (dict(T=7), sv.SPEC_EINVAL),
+         (dict(N=0), sv.SPEC_EINVAL), (dict(cu=P[8]), sv.SPEC_EINVAL), (dict(G=0), sv.SPEC_EINVAL),
+         (dict(rot=63), sv.SPEC_EINVAL), (dict(rot=66), sv.SPEC_EINVAL), (dict(rot=-2), sv.SPEC_EINVAL),
+         (dict(eps=-1.0), sv.SPEC_EINVAL), (dict(eps=float("nan")), sv.SPEC_EINVAL), (dict(D=60), sv.SPEC_EINVAL),
+         (dict(D=264, qs=2112, ks=528, vs=528), sv.SPEC_ECAPACITY), (dict(ks=120), sv.SPEC_EINVAL),
+         (dict(vs=129), sv.SPEC_EINVAL), (dict(k=ODD), sv.SPEC_EINVAL), (dict(out=P[3]), sv.SPEC_EINVAL),
+         (dict(kv=P[1]), sv.SPEC_EINVAL), (dict(st=P[5]), sv.SPEC_EINVAL), (dict(layer=1), sv.SPEC_EINVAL),
+         (dict(dt=9), sv.SPEC_EINVAL)]
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", ROPES + RECT)
+def test_rope_refusals(kw, code):
+    assert LIB.spec_norm_rope_kv(*_args(ROPE, **kw)) == code
+
+
+@needs_lib
+@pytest.mark.parametrize("kw,code", ROPES + PAGES)
+def test_rope_paged_refusals(kw, code):
+    assert LIB.spec_norm_rope_kv_paged(*_args(ROPE_P, **kw)) == code
+
+
+@needs_lib
+def test_workspace_query():
+    f = sv.spec_tree_attention_workspace_bytes
+    assert f(2, 1, 8, 4, 128, 4096, sv.SPEC_BF16) > 0 and f(2, 1, 8, 4, 128, 4096, sv.SPEC_BF16) % 256 == 0
+    assert f(2, 1, 8, 4, 128, 64, sv.SPEC_BF16) == 0                    # one workgroup walks 64 rows
+    for bad in [(0, 1, 8, 4, 128, 64), (1, 0, 8, 4, 128, 64), (1, 257, 8, 4, 128, 64), (1, 1, 0, 4, 128, 64),
+                (1, 1, 8, 0, 128, 64), (1, 1, 8, 4, 257, 64), (1, 1, 8, 4, 128, 0)]:
+        assert f(*bad, sv.SPEC_BF16) == 0
+    assert f(2, 1, 8, 4, 128, 4096, 7) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    kv = torch.zeros(1, 2, 2, 2, 8, 64)
+    q = torch.zeros(2, 3, 4, 64)
+    with pytest.raises(ValueError, match="no whole group"):
+        sv.spec_tree_attention(torch.zeros(2, 3, 3, 64), kv, 0, None, None, q, None)
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        sv.spec_tree_attention(q, kv, 0, None, None, q, None)
+    with pytest.raises(ValueError, match="must be torch.float32"):
+        sv.spec_tree_attention(q.bfloat16(), kv, 0, None, None, q, None)
+    with pytest.raises(ValueError, match=r"\[B, N, heads, D\]"):
+        sv.spec_tree_attention(q[0], kv, 0, None, None, q, None)
+    with pytest.raises(ValueError, match=r"\[L, 2, planes, H, cols, D\]"):
+        sv.spec_prompt_attention(q[0], kv[0], 0, None, None, None, q)
+    with pytest.raises(ValueError, match="must be"):
+        sv.spec_norm_rope_kv(q, q[:, :, :2, :32], q[:, :, :2], kv, 0, None, None, q)

@@ -1,0 +1,176 @@
+"""Norms, rotation and the cache write against the oracle in float64; every
+cell that the call does not own keeps its bits."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import speculative_decoding_verification_04_amd as sv
+from tests._attn import EPS32, HALF, Cache, assert_within, dev, f64, randn
+from tests._gpu import DEV, i32, note, requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+FAR = 1 << 20
+
+
+def _freq(half):
+    return (10000.0 ** (-np.arange(half) / max(half, 1))).astype(np.float32)
+
+
+def _case(seed, dt, H, G, D, lens, new, page, rot, near=False, norm=True, packed=False, positions=None, L=2,
+          fused=True, eps=1e-5):
+    """lens: cached rows (packed: rows with the prompt); new: tokens per sequence."""
+    rng = np.random.default_rng(seed)
+    lens, new = np.asarray(lens), np.asarray(new)
+    B, T = len(lens), int(new.sum())
+    rows = lens if packed else lens + new
+    cache = Cache(rng, dt, L, H, D, rows, lens, page)
+    layer = L - 1
+    row0 = rows - new
+    seq = np.repeat(np.arange(B), new)
+    row = np.concatenate([row0[b] + np.arange(new[b]) for b in range(B)]).astype(np.int64)
+    qkv = randn(rng, dt, T, (G + 2) * H, D, sd=3.0)
+    wq, wk = (randn(rng, dt, D), randn(rng, dt, D)) if norm else (None, None)
+    freq = _freq(rot // 2)
+    at = row if positions is None else positions[:T]
+    d = dev(qkv)
+    q, k, v = d[:, :G * H], d[:, G * H:(G + 1) * H], d[:, (G + 1) * H:]
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    kv, q_out = dev(cache.kv), torch.full((T, G * H, D), 9.0, dtype=qkv.dtype, device=DEV)
+    st = torch.full((B,), -7, dtype=torch.int32, device=DEV)
+    args = (q, k, v, kv, layer, cache.where(), i32(lens), q_out)
+    more = dict(cu_seqlens=i32(np.concatenate([[0], np.cumsum(new)])) if packed else None,
+                positions=None if positions is None else i32(positions[:T]), eps=eps, interleaved=near, status=st,
+                q_weight=None if wq is None else dev(wq), k_weight=None if wk is None else dev(wk),
+                inv_freq=torch.from_numpy(freq).to(DEV) if rot else None)
+    (sv.spec_norm_rope_kv_paged if page else sv.spec_norm_rope_kv)(*args, **more)
+    torch.cuda.synchronize()
+    assert st.cpu().tolist() == [0] * B
+    x = f64(qkv)
+    # Float32 between load and store: the mean of D squares is off by (D + 4) 2^-24 relatively, the
+    # angle's cosine and sine by 2^-21 at most, and each result is a sum of two products.
+    for got, ref, w in ((q_out, x[:, :G * H], wq), (None, x[:, G * H:(G + 1) * H], wk)):
+        want = oracle.norm_rope(ref, None if w is None else f64(w), eps, at, freq, near)
+        size = np.abs(oracle.norm_rope(ref, None if w is None else f64(w), eps, at, freq[:0], near)).max(-1, keepdims=True)
+        tol = (D + 32) * EPS32 * size + 1.01 * HALF[dt] * np.abs(want)
+        if got is None:
+            got = np.stack([f64(kv[layer, 0])[p, :, c] for p, c in (cache.places[b][r] for b, r in zip(seq, row))])
+        assert_within(got, want, tol)
+    expect = cache.kv.clone()
+    for t, (b, r) in enumerate(zip(seq, row)):
+        p, c = cache.places[b][r]
+        expect[layer, 1, p, :, c] = qkv[t, (G + 1) * H:]
+        expect[layer, 0, p, :, c] = kv[layer, 0, p, :, c].cpu()
+    bits = torch.int16 if dt == "bf16" else torch.int32
+    assert torch.equal(expect.view(bits), kv.cpu().view(bits))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H,G,D,rot", [(1, 1, 8, 8), (2, 3, 64, 64), (8, 4, 128, 128), (2, 7, 80, 80), (2, 2, 80, 40),
+                                       (1, 8, 256, 256), (3, 1, 96, 22), (4, 2, 64, 0), (2, 2, 192, 128)])
+def test_slots_of_the_verify_forward(dt, H, G, D, rot):
+    for page in (0, 7):
+        note(f"norm rope {dt} H={H} G={G} D={D} rot={rot} page={page}")
+        _case(D + G, dt, H, G, D, [0, 5, 33], [3, 3, 3], page, rot)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,rot", [(64, 64), (80, 40), (96, 22), (256, 128)])
+def test_neighbouring_pairs(dt, D, rot):
+    note(f"norm rope interleaved {dt} D={D} rot={rot}")
+    _case(D, dt, 2, 2, D, [4, 1], [5, 5], 4, rot, near=True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [0, 16])
+def test_packed_prompts(dt, page):
+    # a whole prompt, one of no tokens, one token, a chunk behind cached rows
+    note(f"norm rope prompts {dt} page={page}")
+    _case(3, dt, 2, 4, 128, [50, 9, 1, 40], [50, 0, 1, 13], page, 128, packed=True)
+
+
+def test_many_sequences_are_found():
+    note("norm rope 200 prompts")
+    rng = np.random.default_rng(5)
+    new = rng.integers(0, 4, 200)
+    _case(4, "bf16", 1, 1, 64, new + rng.integers(0, 3, 200) + (new == 0), new, 0, 64, packed=True)
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_far_positions_without_norm(fused):
+    note("norm rope far positions")
+    pos = np.array([0, 1, FAR, FAR + 1, 2 ** 31 - 1, 12345, 7, 8])
+    _case(6, "f32", 2, 2, 64, [3, 9], [4, 4], 0, 64, norm=False, positions=pos, fused=fused)
+
+
+def test_one_token_zero_head_and_eps():
+    note("norm rope zero head")
+    q = torch.zeros(1, 2, 64, device=DEV)
+    kv = torch.full((1, 2, 1, 1, 4, 64), 5.0, device=DEV)
+    out, w = torch.empty(1, 2, 64, device=DEV), torch.ones(64, device=DEV)
+    sv.spec_norm_rope_kv(q, q[:, :1], q[:, :1], kv, 0, i32([2]), i32([0]), out, q_weight=w, k_weight=w, eps=1e-6)
+    assert float(out.abs().max()) == 0.0 and float(kv[0, :, 0, 0, 2].abs().max()) == 0.0
+    assert float(kv[0, :, 0, 0, [0, 1, 3]].min()) == 5.0
+
+
+def test_states_out_of_range_write_nothing():
+    """n > E, n < 0 and a bad page: that sequence's cache keeps its bits and its status says so;
+    the others are served."""
+    H, D, N = 2, 64, 2
+    gen = torch.Generator().manual_seed(0)
+    x = torch.randn(3 * N, 4 * H, D, generator=gen).to(DEV)
+    q, k, v = x[:, :2 * H], x[:, 2 * H:3 * H], x[:, 3 * H:]
+    out = torch.empty(3 * N, 2 * H, D, device=DEV)
+    st = torch.full((3,), -7, dtype=torch.int32, device=DEV)
+    note("norm rope bad states")
+    kv = torch.zeros(1, 2, 3, H, 8, D, device=DEV)
+    sv.spec_norm_rope_kv(q, k, v, kv, 0, i32([5]), i32([6, 3, -1]), out, status=st)
+    assert st.cpu().tolist() == [sv.SPEC_ST_BAD_STATE, 0, sv.SPEC_ST_BAD_STATE]
+    assert float(kv[:, :, [0, 2]].abs().max()) == 0.0 and torch.equal(kv[0, 1, 1, :, 5:7], v[N:2 * N].transpose(0, 1))
+    kv.zero_()
+    sv.spec_norm_rope_kv(q, k, v, kv, 0, i32([7]), i32([6, 3, 1]), out, status=st)         # 7 + 2 > 8
+    assert st.cpu().tolist() == [sv.SPEC_ST_CAPACITY] * 3 and float(kv.abs().max()) == 0.0
+    pool = torch.zeros(1, 2, 4, H, 2, D, device=DEV)
+    table = i32([[0, 1], [2, 4], [3, -1]])
+    sv.spec_norm_rope_kv_paged(q, k, v, pool, 0, table, i32([1, 2, 3]), out, status=st)
+    assert st.cpu().tolist() == [0, sv.SPEC_ST_BAD_STATE, sv.SPEC_ST_CAPACITY]
+    assert float(pool[:, :, [2, 3]].abs().max()) == 0.0 and torch.equal(pool[0, 1, 1, :, 0], v[1])
+    # malformed prompt ranges: sequence 1 runs backwards, tokens of no sequence are left alone
+    out.fill_(3.0)
+    kv.zero_()
+    sv.spec_norm_rope_kv(q, k, v, kv, 0, i32([6]), i32([2, 2, 2]), out, cu_seqlens=i32([0, 2, 1, 9]), status=st)
+    assert st.cpu().tolist() == [0, sv.SPEC_ST_BAD_STATE, sv.SPEC_ST_BAD_STATE]
+    assert float(kv[:, :, 1:].abs().max()) == 0.0
+    out.fill_(3.0)
+    sv.spec_norm_rope_kv(q, k, v, kv, 0, i32([6]), i32([2, 2, 0]), out, cu_seqlens=i32([0, 2, 4, 4]), status=st)
+    assert st.cpu().tolist() == [0, 0, 0] and bool((out[4:] == 3.0).all()) and not bool((out[:4] == 3.0).any())
+
+
+def test_graph_replay_and_side_stream():
+    rng = np.random.default_rng(8)
+    x = dev(randn(rng, "bf16", 12, 6, 64))
+    kv = torch.zeros(1, 2, 4, 1, 9, 64, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty(12, 4, 64, dtype=torch.bfloat16, device=DEV)
+    E, n, f = i32([5]), i32([0, 5, 2, 3]), torch.from_numpy(_freq(32)).to(DEV)
+    call = lambda: sv.spec_norm_rope_kv(x[:, :4], x[:, 4:5], x[:, 5:], kv, 0, E, n, out, inv_freq=f)  # noqa: E731
+    note("norm rope graph")
+    call()
+    torch.cuda.synchronize()
+    want = out.clone(), kv.clone()
+    side = torch.cuda.Stream()
+    out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    sv.spec_norm_rope_kv(x[:, :4], x[:, 4:5], x[:, 5:], kv, 0, E, n, out, inv_freq=f, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        out.zero_()
+        kv.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(kv, want[1])

@@ -74,12 +74,11 @@ struct Shape {
   static constexpr int kNB = RW == 4 && kElt == 2 ? 2 : 1;
   static constexpr int kKT = 32 * kNB * kKW;
   static constexpr int kChunks = DP / kVec;               // 16-byte chunks in a row
-  static constexpr int kRowsPass = kThreads / kChunks;    // rows the workgroup loads at once
-  static constexpr int kLoads = kKT / kRowsPass;
+  static constexpr int kLoads = kKT * kChunks / kThreads; // chunks of K (or V) that a lane brings
   static constexpr int kTile = kKT * DP * kElt;           // bytes of K (or V)
-  static constexpr int kJoin = (kKW - 1) * RW * 32 * (DP + 2) * 4;
-  static constexpr int kLds = 2 * kTile > kJoin ? 2 * kTile : kJoin;
-  static_assert(kRowsPass * kLoads == kKT, "whole passes");
+  static constexpr int kLds = 2 * kTile;                  // of one buffer
+  static constexpr int kJoin = (kKW - 1) * RW * 32 * DP * 4;
+  static_assert(kLoads * kThreads == kKT * kChunks && kJoin <= kLds && 2 * kLds <= 160 * 1024 - 2048, "LDS");
 };
 
 // LDS place of chunk c of row r.  Rows of 256 bytes and more all start at bank
@@ -88,11 +87,15 @@ struct Shape {
 // sixteen rows (a read of K) sixteen different chunks.  Rows of 128 bytes
 // start at two places, and eight chunks serve two rows each.
 template <int CHUNKS>
-__device__ inline int place(int r, int c) {
+__device__ inline int turn(int r) {
   if constexpr (CHUNKS >= 16)
-    return r * CHUNKS + (c ^ (((r & 3) << 2) | ((r >> 2) & 3)));
+    return ((r & 3) << 2) | ((r >> 2) & 3);
   else
-    return r * CHUNKS + (c ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3)));
+    return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+template <int CHUNKS>
+__device__ inline int place(int r, int c) {
+  return r * CHUNKS + (c ^ turn<CHUNKS>(r));
 }
 
 __device__ inline float half_max(float x) {
@@ -115,11 +118,6 @@ __device__ inline bf16x4b read_turned(const char *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds) const_cast<char *>(p));
 }
 
-// Whether a word of two bf16 values holds an infinity or a NaN.
-__device__ inline bool odd2(uint32_t w) {
-  return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
-}
-
 // The state of one wave's 32 query rows.
 template <typename T, int DP>
 struct Rows {
@@ -131,24 +129,25 @@ struct Rows {
   uint32_t sees;              // trees: any bit of the row's mask
 };
 
-// Loads of one K and V tile into registers, and their store to LDS.
+// Brings K and V tiles from the cache straight into LDS.  A wave's load writes
+// 64 consecutive 16-byte places, so the lane takes the chunk whose place its
+// own is.  Chunks past D are never loaded: they stay zero (clear()).
 template <typename T, int DP, int RW, bool PAGED>
 struct Loader {
   using S = Shape<T, DP, RW>;
   const Params &P;
   const Job &J;
-  int chunk, row;
-  bool in;
   int page[S::kLoads];
   int bad;
-  u32x4 k[S::kLoads], v[S::kLoads];
 
-  __device__ Loader(const Params &p, const Job &j) : P(p), J(j), bad(0) {
-    chunk = threadIdx.x % S::kChunks;
-    row = threadIdx.x / S::kChunks;
-    in = chunk * S::kVec < P.c.D;
+  __device__ Loader(const Params &p, const Job &j) : P(p), J(j), bad(0) {}
+  static __device__ int row(int i) { return (i * kThreads + threadIdx.x) / S::kChunks; }
+  static __device__ int chunk(int i) { return threadIdx.x % S::kChunks ^ turn<S::kChunks>(row(i)); }
+  __device__ int at(int t, int i) const { return min(t * S::kKT + row(i), J.total - 1); }
+  __device__ void clear(char *buf) const {
+    if (P.c.D == DP) return;
+    for (int x = threadIdx.x; x < S::kLds / 16; x += kThreads) reinterpret_cast<u32x4 *>(buf)[x] = u32x4{0, 0, 0, 0};
   }
-  __device__ int at(int t, int i) const { return min(t * S::kKT + i * S::kRowsPass + row, J.total - 1); }
   __device__ void pages(int t) {
     if constexpr (PAGED) {
 #pragma unroll
@@ -156,7 +155,10 @@ struct Loader {
         page[i] = P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, at(t, i))];
     }
   }
-  __device__ void load(int t) {
+  __device__ void load(int t, char *buf) {
+    typedef __attribute__((address_space(3))) char *Lds;
+    typedef const __attribute__((address_space(1))) char *Global;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int r = at(t, i);
@@ -165,25 +167,43 @@ struct Loader {
         plane = page[i];
         col = r - cache_page(P.c, r) * P.c.cols;
         if (plane < 0 || plane >= P.c.planes) {
-          bad = SPEC_ST_BAD_STATE;
+          bad = 1;
           plane = 0;
         }
       }
-      const long long off = cache_offset(P.c, plane, J.h, col, S::kElt) + chunk * 16;
-      k[i] = v[i] = u32x4{0, 0, 0, 0};
-      if (in) {
-        k[i] = *reinterpret_cast<const u32x4 *>(P.c.k + off);
-        v[i] = *reinterpret_cast<const u32x4 *>(P.c.v + off);
+      const int c = chunk(i);
+      if (DP == P.c.D || c * S::kVec < P.c.D) {
+        const long long off = cache_offset(P.c, plane, J.h, col, S::kElt) + c * 16;
+        char *to = buf + (i * kThreads + wave * kWave) * 16;
+        __builtin_amdgcn_global_load_lds((Global)(P.c.k + off), (Lds)to, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((Global)(P.c.v + off), (Lds)(to + S::kTile), 16, 0, 0);
       }
     }
   }
-  __device__ void store(char *lds) const {
+  // Takes infinities and NaNs out of the lane's own chunks of a V tile.
+  __device__ bool clean(char *buf) const {
+    bool found = false;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      const int at = place<S::kChunks>(i * S::kRowsPass + row, chunk) * 16;
-      *reinterpret_cast<u32x4 *>(lds + at) = k[i];
-      *reinterpret_cast<u32x4 *>(lds + S::kTile + at) = v[i];
+      u32x4 *at = reinterpret_cast<u32x4 *>(buf + S::kTile) + i * kThreads + threadIdx.x;
+      u32x4 x = *at;
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (S::kElt == 2) {
+          const bool lo = (x[j] & 0x7f80u) == 0x7f80u, hi = (x[j] & 0x7f800000u) == 0x7f800000u;
+          any |= lo | hi;
+          x[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+        } else {
+          const bool odd = (x[j] & 0x7f800000u) == 0x7f800000u;
+          any |= odd;
+          if (odd) x[j] = 0;
+        }
+      }
+      if (any) *at = x;
+      found |= any;
     }
+    return found;
   }
 };
 
@@ -209,43 +229,53 @@ __device__ inline uint32_t seen(const Params &P, const Job &J, int token, int k0
   return (bits | cached) & valid;
 }
 
+// A value that the compiler takes for new: what is computed from it stays in
+// the loop.  Two dozen LDS addresses kept across the loop instead cost more
+// registers than the wave has beside its tiles, and an xor each is free.
+__device__ inline int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // One tile: the wave's scores, the softmax step and the second product.
 // kb0: the wave's first cache row in the tile; vis: seen() of its blocks.
+// turn() is the same for rows 16 apart and differs by 2 for rows 8 apart, so
+// all of a lane's places are one offset, with an xor of constant bits for the
+// chunk and a constant distance for the row.
 template <typename T, int DP, int RW, bool MASKED>
 __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
                             const uint32_t (&vis)[Shape<T, DP, RW>::kNB]) {
   using S = Shape<T, DP, RW>;
+  constexpr int kRow = DP * S::kElt;
   const int lane = threadIdx.x & (kWave - 1), n = lane & 31, hf = lane >> 5;
   const char *ldk = lds, *ldv = lds + S::kTile;
   f32x16 s[S::kNB];
+  const int ka = fresh((kb0 + n) * kRow + ((hf ^ turn<S::kChunks>(n)) << 4));
 #pragma unroll
   for (int nb = 0; nb < S::kNB; ++nb) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[nb][r] = 0.0f;
-    const int row = kb0 + nb * 32 + n;
     if constexpr (S::kElt == 2) {
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(ldk + place<S::kChunks>(row, 2 * d + hf) * 16);
+        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(ldk + (ka ^ (d << 5)) + nb * 32 * kRow);
         s[nb] = mfma(a, W.q[d], s[nb]);
       }
     } else {
 #pragma unroll
       for (int d = 0; d < DP / 8; ++d) {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(ldk + place<S::kChunks>(row, 2 * d + hf) * 16);
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(ldk + (ka ^ (d << 5)) + nb * 32 * kRow);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], W.q[d][j], s[nb], 0, 0, 0);
       }
     }
   }
-  uint32_t see[S::kNB];
   if constexpr (MASKED) {
 #pragma unroll
     for (int nb = 0; nb < S::kNB; ++nb) {
-      see[nb] = vis[nb] >> (4 * hf);
+      const uint32_t see = vis[nb] >> (4 * hf);
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        s[nb][r] = (see[nb] >> (8 * (r / 4) + r % 4)) & 1u ? s[nb][r] : -INFINITY;
+      for (int r = 0; r < 16; ++r) s[nb][r] = (see >> (8 * (r / 4) + r % 4)) & 1u ? s[nb][r] : -INFINITY;
     }
   }
   float mx = s[0][0];
@@ -271,69 +301,68 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
 #pragma unroll
     for (int r = 0; r < 16; ++r) W.o[db][r] *= alpha;
 
-  // O^T += V^T P^T.  In masked tiles V rows that a query does not see may hold
-  // anything, and 0 * inf is not 0: infinities and NaNs are taken out of the
-  // operand and added by a product of their own with the rows' visibility.
+  // O^T += V^T P^T
   if constexpr (S::kElt == 2) {
-    const int i = lane & 15, dg = (lane >> 4) & 1;
+    const int i = lane & 15, dg = (lane >> 4) & 1, r0 = 4 * hf + (i >> 2);
+    const int va = fresh((kb0 + r0) * kRow + (((2 * dg + ((i & 3) >> 1)) ^ turn<S::kChunks>(r0)) << 4) + (i & 1) * 8);
 #pragma unroll
     for (int t = 0; t < 2 * S::kNB; ++t) {
       bf16x8 p;
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = static_cast<__bf16>(s[t / 2][8 * (t % 2) + j]);
-      const int r0 = kb0 + 16 * t + 4 * hf + (i >> 2);
 #pragma unroll
       for (int db = 0; db < DP / 32; ++db) {
-        const int c = 4 * db + 2 * dg + ((i & 3) >> 1), e = (i & 1) * 8;
-        const bf16x4b lo = read_turned(ldv + place<S::kChunks>(r0, c) * 16 + e);
-        const bf16x4b hi = read_turned(ldv + place<S::kChunks>(r0 + 8, c) * 16 + e);
-        bf16x8 a = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if constexpr (MASKED) {
-          u32x4 w = __builtin_bit_cast(u32x4, a);
-          if (__any(odd2(w[0]) || odd2(w[1]) || odd2(w[2]) || odd2(w[3]))) {
-            bf16x8 up, down, vs;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float x = static_cast<float>(a[j]);
-              const bool nan = x != x;
-              up[j] = static_cast<__bf16>(nan || x == INFINITY ? 1.0f : 0.0f);
-              down[j] = static_cast<__bf16>(nan || x == -INFINITY ? 1.0f : 0.0f);
-              if (nan || fabsf(x) == INFINITY) a[j] = static_cast<__bf16>(0.0f);
-              const int r = 8 * (t % 2) + j;
-              vs[j] = static_cast<__bf16>((see[t / 2] >> (8 * (r / 4) + r % 4)) & 1u ? 1.0f : 0.0f);
-            }
-            f32x16 z = {};
-            const f32x16 u = mfma(up, vs, z), d = mfma(down, vs, z);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) W.o[db][r] += (u[r] > 0 ? INFINITY : 0.0f) + (d[r] > 0 ? -INFINITY : 0.0f);
-          }
-        }
+        const bf16x4b lo = read_turned(ldv + (va ^ (db << 6)) + 16 * t * kRow);
+        const bf16x4b hi = read_turned(ldv + (va ^ (db << 6 | 2 << 4)) + (16 * t + 8) * kRow);
+        const bf16x8 a = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         W.o[db] = mfma(a, p, W.o[db]);
       }
     }
   } else {
+    const int va = fresh((kb0 + 4 * hf) * kRow + ((n / 4 ^ hf) << 4) + n % 4 * 4);
 #pragma unroll
     for (int r = 0; r < 16 * S::kNB; ++r) {
-      const int row = kb0 + 32 * (r / 16) + 8 * (r % 16 / 4) + 4 * hf + r % 4;
       const float p = s[r / 16][r % 16];
+      const int row = 32 * (r / 16) + 8 * (r % 16 / 4) + r % 4;
 #pragma unroll
       for (int db = 0; db < DP / 32; ++db) {
-        float a = *reinterpret_cast<const float *>(ldv + place<S::kChunks>(row, 8 * db + n / 4) * 16 + n % 4 * 4);
-        if constexpr (MASKED) {
-          if (__any(!(fabsf(a) < INFINITY))) {
-            const float up = a == INFINITY || a != a ? 1.0f : 0.0f, down = a == -INFINITY || a != a ? 1.0f : 0.0f;
-            const float vs = (see[r / 16] >> (8 * (r % 16 / 4) + r % 4)) & 1u ? 1.0f : 0.0f;
-            if (!(fabsf(a) < INFINITY)) a = 0.0f;
-            f32x16 z = {};
-            const f32x16 u = __builtin_amdgcn_mfma_f32_32x32x2f32(up, vs, z, 0, 0, 0);
-            const f32x16 d = __builtin_amdgcn_mfma_f32_32x32x2f32(down, vs, z, 0, 0, 0);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) W.o[db][x] += (u[x] > 0 ? INFINITY : 0.0f) + (d[x] > 0 ? -INFINITY : 0.0f);
-          }
-        }
+        const float a = *reinterpret_cast<const float *>(ldv + (va ^ (db << 7) ^ (turn<S::kChunks>(row) << 4)) + row * kRow);
         W.o[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p, W.o[db], 0, 0, 0);
       }
     }
+  }
+}
+
+// In tiles that some rows do not see whole, V rows may hold anything where they
+// are not seen, and 0 * inf is not 0.  Such a tile's infinities and NaNs are
+// zero in LDS (clean()); here they are added to the query rows that see them,
+// from the cache itself.  Rare: one row of the cache after the other.
+template <typename T, int DP, int RW, bool PAGED>
+__device__ inline void add_odd(const Params &P, const Job &J, Rows<T, DP> &W, int k0,
+                               const uint32_t (&vis)[Shape<T, DP, RW>::kNB]) {
+  using S = Shape<T, DP, RW>;
+  const int hf = (threadIdx.x & (kWave - 1)) >> 5;
+  for (int j = 0; j < 32 * S::kNB; ++j) {
+    const int r = k0 + j;
+    if (r >= J.total) break;
+    uint32_t word = vis[0];
+    if constexpr (S::kNB == 2) word = j < 32 ? vis[0] : vis[1];
+    const bool see = (word >> (j & 31)) & 1u;
+    int plane = J.b, col = J.start_col + r;
+    if constexpr (PAGED) {
+      plane = P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, r)];
+      if (plane < 0 || plane >= P.c.planes) plane = 0;
+      col = r - cache_page(P.c, r) * P.c.cols;
+    }
+    const T *v = reinterpret_cast<const T *>(P.c.v + cache_offset(P.c, plane, J.h, col, S::kElt));
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int d = 32 * db + 8 * (i / 4) + 4 * hf + i % 4;
+        const float x = d < P.c.D ? static_cast<float>(v[d]) : 0.0f;
+        if (see && !(fabsf(x) < INFINITY)) W.o[db][i] += x;
+      }
   }
 }
 
@@ -353,7 +382,7 @@ __device__ inline void put4(char *out, int d0, int D, const float (&x)[4]) {
 
 // The whole walk of one job.  slot < 0: outputs are final; else partials.
 template <typename T, int DP, int RW, bool PAGED, bool PROMPT>
-__device__ inline int walk(const Params &P, const Job &J, long long slot, char *lds) {
+__device__ inline int walk(const Params &P, const Job &J, long long slot, char *buf0, char *buf1) {
   using S = Shape<T, DP, RW>;
   const int lane = threadIdx.x & (kWave - 1), n = lane & 31, hf = lane >> 5;
   const int wave = threadIdx.x / kWave, rw = wave % RW, kw = wave / RW;
@@ -386,36 +415,60 @@ __device__ inline int walk(const Params &P, const Job &J, long long slot, char *
   // cache rows below `plain` are seen by every row of the workgroup
   const int plain = !PROMPT && P.mask ? J.limit0 - 1 : J.limit0 + J.row0 / P.G;
   Loader<T, DP, RW, PAGED> ld(P, J);
+  ld.clear(buf0);
+  ld.clear(buf1);
+  if (P.c.D != DP) __syncthreads();
   if (J.t0 < J.t1) {
     ld.pages(J.t0);
-    ld.load(J.t0);
+    ld.load(J.t0, buf0);
     ld.pages(min(J.t0 + 1, J.t1 - 1));
   }
-  for (int t = J.t0; t < J.t1; ++t) {
-    __syncthreads();                                      // the tile before is read
-    ld.store(lds);
+  // Tile t is used from one buffer while tile t + 1 arrives in the other.
+  const int kb0 = kw * 32 * S::kNB;
+  auto begin = [&](int t, char *next) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): this wave's part of tile t is in LDS
+    __syncthreads();                                      // everyone's is, and tile t - 1 is read
     if (t + 1 < J.t1) {
-      ld.load(t + 1);
+      ld.load(t + 1, next);
       ld.pages(min(t + 2, J.t1 - 1));
     }
-    __syncthreads();
-    const int kb0 = kw * 32 * S::kNB, k0 = t * S::kKT + kb0;
-    uint32_t vis[S::kNB] = {};
-    if (t * S::kKT + S::kKT <= plain) {
-      step<T, DP, RW, false>(W, lds, kb0, P.sl, vis);
-    } else {
+  };
+  auto tile = [&](int t, char *now, char *next) __attribute__((always_inline)) {
+    begin(t, next);
+    const uint32_t all[S::kNB] = {};
+    step<T, DP, RW, false>(W, now, kb0, P.sl, all);
+  };
+  int t = J.t0;
+  const int mid = min(J.t1, plain / S::kKT);              // tiles that every row sees whole
+  char *now = buf0, *next = buf1;
+  for (; t + 1 < mid; t += 2) {
+    tile(t, buf0, buf1);
+    tile(t + 1, buf1, buf0);
+  }
+  if (t < mid) {
+    tile(t++, buf0, buf1);
+    now = buf1;
+    next = buf0;
+  }
+  for (; t < J.t1; ++t) {
+    begin(t, next);
+    uint32_t vis[S::kNB];
 #pragma unroll
-      for (int nb = 0; nb < S::kNB; ++nb) vis[nb] = seen<PROMPT>(P, J, token, k0 + 32 * nb);
-      step<T, DP, RW, true>(W, lds, kb0, P.sl, vis);
-    }
+    for (int nb = 0; nb < S::kNB; ++nb) vis[nb] = seen<PROMPT>(P, J, token, t * S::kKT + kb0 + 32 * nb);
+    const bool odd = __syncthreads_or(ld.clean(now));
+    step<T, DP, RW, true>(W, now, kb0, P.sl, vis);
+    if (odd) add_odd<T, DP, RW, PAGED>(P, J, W, t * S::kKT + kb0, vis);
+    char *x = now;
+    now = next;
+    next = x;
   }
   float l = half_sum(W.l), m = W.m;
   // Join the waves that shared the rows: each brings its maximum, sum and
   // output; the first adds them, scaled to the common maximum.
   if constexpr (S::kKW > 1) {
     __syncthreads();
-    float *jo = reinterpret_cast<float *>(lds);           // [kw - 1][rw][DP][32]
-    float *jm = jo + (S::kKW - 1) * RW * 32 * DP;         // [kw - 1][rw][2][32]
+    float *jo = reinterpret_cast<float *>(buf0);          // [kw - 1][rw][DP][32]
+    __shared__ float jm[(S::kKW - 1) * RW * 64];          // [kw - 1][rw][2][32]
     if (kw > 0) {
       float *o = jo + ((kw - 1) * RW + rw) * 32 * DP;
 #pragma unroll

@@ -68,7 +68,8 @@ __device__ inline Where find_tile(const Params &P, int f) {
 template <typename T, int DP, bool PAGED>
 __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void prompt_kernel(Params P) {
   using S = Shape<T, DP, kRW>;
-  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
+  __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
   const int H = P.c.H;
   const int h = blockIdx.x % H, f = blockIdx.x / H;
   if (blockIdx.x == 0 && P.status) {
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
   const int last = min((J.row0 + kTileRows - 1) / P.G, len - 1);      // the tile's last token
   J.t0 = 0;
   J.t1 = (J.limit0 + last + S::kKT - 1) / S::kKT;
-  const int bad = walk<T, DP, kRW, PAGED, true>(P, J, -1, lds);
+  const int bad = walk<T, DP, kRW, PAGED, true>(P, J, -1, buf0, buf1);
   if (reports && threadIdx.x == 0) P.status[w.b] = bad;
 }
 

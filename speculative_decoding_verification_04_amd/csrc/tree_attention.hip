@@ -22,10 +22,12 @@ struct Plan {
   long long slots;
 };
 
-inline Plan plan_of(int B, int N, int H, int G, long long max_rows, spec_dtype dt) {
+inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_dtype dt) {
   Plan p;
   const long long R = static_cast<long long>(N) * G;
-  p.rw = R > 64 ? 4 : R > 32 || dt == SPEC_F32 ? 2 : 1;
+  // two buffers of a tile fit LDS: 32 * 4 / rw cache rows of K and V (64 for bf16 and rw = 4)
+  const int least = (dt == SPEC_F32 ? 2 : 1) * (D > 128 ? 2 : 1);
+  p.rw = R > 64 || least == 4 ? 4 : R > 32 || least == 2 ? 2 : 1;
   p.tile_rows = 32 * p.rw;
   p.row_tiles = static_cast<int>((R + p.tile_rows - 1) / p.tile_rows);
   const long long groups = static_cast<long long>(B) * H * p.row_tiles;
@@ -62,7 +64,8 @@ __device__ inline int tree_status(const Params &P, int b) {
 template <typename T, int DP, int RW, bool PAGED>
 __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void tree_kernel(Params P) {
   using S = Shape<T, DP, RW>;
-  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
+  __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
   const int x = blockIdx.x;                               // ((b * H + h) * row_tiles + rt) * splits + s
   const int s = x % P.splits, y = x / P.splits, rt = y % P.row_tiles, bh = y / P.row_tiles;
   Job J;
@@ -86,7 +89,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
   const int tiles = (J.total + S::kKT - 1) / S::kKT;
   J.t0 = static_cast<int>(static_cast<long long>(tiles) * s / P.splits);
   J.t1 = static_cast<int>(static_cast<long long>(tiles) * (s + 1) / P.splits);
-  const int bad = walk<T, DP, RW, PAGED, false>(P, J, P.splits > 1 ? x : -1, lds);
+  const int bad = walk<T, DP, RW, PAGED, false>(P, J, P.splits > 1 ? x : -1, buf0, buf1);
   if (threadIdx.x == 0) {
     if (P.splits > 1)
       P.part_bad[x] = bad;
@@ -159,8 +162,10 @@ template <typename T, int DP>
 void launch_tree(const Params &P, const Plan &p, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.slots);
   if (p.rw == 4) return launch_rows<T, DP, 4>(P, grid, s);
-  if (p.rw == 2) return launch_rows<T, DP, 2>(P, grid, s);
-  if constexpr (sizeof(T) == 2) launch_rows<T, DP, 1>(P, grid, s);
+  if constexpr (sizeof(T) * DP <= 512) {
+    if (p.rw == 2) return launch_rows<T, DP, 2>(P, grid, s);
+  }
+  if constexpr (sizeof(T) * DP <= 256) launch_rows<T, DP, 1>(P, grid, s);
 }
 
 template <typename T>
@@ -193,7 +198,7 @@ int tree_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, in
   if (!aligned(mask, 4)) return SPEC_EINVAL;
   const long long tokens = static_cast<long long>(B) * N;
   if (tokens * H * G >= INT32_MAX) return SPEC_EINVAL;
-  const Plan p = plan_of(B, N, H, G, cache_capacity(P.c), dt);
+  const Plan p = plan_of(B, N, H, G, D, cache_capacity(P.c), dt);
   if (p.slots >= INT32_MAX) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const int words = (N + 31) / 32;
@@ -239,7 +244,7 @@ extern "C" size_t spec_tree_attention_workspace_bytes(int B, int N, int H, int G
   if (dt != SPEC_F32 && dt != SPEC_BF16) return 0;
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return 0;
   if (static_cast<long long>(B) * N * H * G >= INT32_MAX) return 0;
-  return part_bytes(plan_of(B, N, H, G, max_rows, dt), D);
+  return part_bytes(plan_of(B, N, H, G, D, max_rows, dt), D);
 }
 
 extern "C" int spec_tree_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B, int H,

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import _lib
 
 SPEC_F32, SPEC_BF16 = 0, 1
@@ -93,13 +95,11 @@ def _same(t, ref, name: str):
 
 
 def _stream(stream):
-    import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
 
 def _dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.bfloat16:
         return SPEC_BF16
     if t.dtype == torch.float32:
@@ -112,7 +112,6 @@ def workspace(nbytes: int, device=None):
     stochastic verification need a zero-filled workspace that no other kind
     of call writes into (they keep it zero-filled between calls); the other
     calls ignore the contents."""
-    import torch
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -361,82 +360,115 @@ def spec_group_same_length(lengths, B: int, min_group: int, perm, batch_start, b
     _check(code, "spec_group_same_length")
 
 
+def _place(t, stream):
+    """Device index of a call whose main tensor is t, and the stream it runs on: the library launches
+    on the current device, so the tensors have to be there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensor must be on the GPU")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev, (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _need(t, dtype, numel: int, name: str, dev: int, optional: bool = False):
+    """Address of an argument tensor after _arg's checks, and that it is on the call's device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} needs at least {numel} elements, has {t.numel()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def spec_tree_mask(first_child, next_sibling, kv_len, positions, mask, *, status=None, stream=None) -> None:
     """first_child, next_sibling [B, N], kv_len [B] int32; positions [B, N] int32 out, mask
     [B, N, ceil(N / 32)] int32 out (bit words), for spec_norm_rope_kv and spec_tree_attention."""
     B, N = first_child.shape
+    i32 = torch.int32
+    dev, s = _place(first_child, stream)
     code = library().spec_tree_mask(
-        B, N, _arg(first_child, "int32", B * N, "first_child"), _arg(next_sibling, "int32", B * N, "next_sibling"),
-        _arg(kv_len, "int32", B, "kv_len"), _arg(positions, "int32", B * N, "positions"),
-        _arg(mask, "int32", B * N * ((N + 31) // 32), "mask"), _arg(status, "int32", B, "status", True),
-        _stream(stream))
+        B, N, _need(first_child, i32, B * N, "first_child", dev), _need(next_sibling, i32, B * N, "next_sibling", dev),
+        _need(kv_len, i32, B, "kv_len", dev), _need(positions, i32, B * N, "positions", dev),
+        _need(mask, i32, B * N * ((N + 31) // 32), "mask", dev), _need(status, i32, B, "status", dev, True), s)
     _check(code, "spec_tree_mask")
 
 
-def _token_rows(t, heads: int, ref, name: str, tokens=None):
-    """Pointer and token stride (elements) of [..., heads, D] rows of ref's dtype and head size:
-    contiguous heads, one stride from token to token (a view of a fused projection will do)."""
-    if t.dtype != ref.dtype:
-        raise ValueError(f"{name} must be {ref.dtype}, not {t.dtype}")
-    D = ref.shape[-1]
-    if t.dim() not in (3, 4) or tuple(t.shape[-2:]) != (heads, D):
-        raise ValueError(f"{name} must be [..., {heads}, {D}], got {tuple(t.shape)}")
-    count = 1
-    for x in t.shape[:-2]:
-        count *= x
-    if tokens is not None and count != tokens:
-        raise ValueError(f"{name} needs {tokens} tokens, has {count}")
-    if not t.is_cuda:
-        raise ValueError("tensor must be on the GPU")
-    step = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else heads * D)
-    if (D > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != D):
+def _token_rows(t, heads: int, kv, D: int, name: str, dev: int, tokens: int = 0):
+    """Address, token stride (elements) and count of [..., heads, D] rows of the cache's dtype: contiguous
+    heads, one stride from token to token (a view of a fused projection will do)."""
+    if t.dtype is not kv.dtype:
+        raise ValueError(f"{name} must be {kv.dtype}, not {t.dtype}")
+    shape, step = t.shape, t.stride()
+    if len(shape) not in (3, 4) or shape[-2] != heads or shape[-1] != D:
+        raise ValueError(f"{name} must be [..., {heads}, {D}], got {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, not {t.device}")
+    if (step[-1] != 1 and D > 1) or (step[-2] != D and heads > 1):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != step * t.shape[1]:
-        raise ValueError(f"{name}: one stride from token to token is needed")
-    return ctypes.c_void_p(t.data_ptr()), int(step), count
+    count, row = shape[-3], step[-3]
+    if len(shape) == 4:
+        if shape[0] > 1:
+            if count == 1:
+                row = step[0]
+            elif step[0] != row * count:
+                raise ValueError(f"{name}: one stride from token to token is needed")
+        count *= shape[0]
+    if tokens and count != tokens:
+        raise ValueError(f"{name} needs {tokens} tokens, has {count}")
+    return t.data_ptr(), row if count > 1 else heads * D, count
 
 
-def _cache_dims(kv, heads: int, G_of: str):
+def _cache_dims(kv, heads: int):
     """Sizes of a cache [L, 2, planes, H, cols, D] and the group size of `heads` query heads."""
-    if kv.dim() != 6 or kv.shape[1] != 2:
+    shape = kv.shape
+    if len(shape) != 6 or shape[1] != 2:
         raise ValueError("the cache must be [L, 2, planes, H, cols, D]")
-    L, _, planes, H, cols, D = kv.shape
+    L, _, planes, H, cols, D = shape
     if heads < H or heads % H:
-        raise ValueError(f"{G_of} has {heads} heads, the cache {H}: no whole group")
+        raise ValueError(f"q has {heads} heads, the cache {H}: no whole group")
+    if not kv.is_contiguous():
+        raise ValueError("the cache must be contiguous")
     return L, planes, H, cols, D, heads // H
 
 
-def _block_table(block_table):
-    B, max_pages = block_table.shape
-    return _arg(block_table, "int32", B * max_pages, "block_table"), B, max_pages
+def _same_size(out, ref, count: int, name: str, dev: int):
+    """Address of an output of exactly `count` elements of ref's dtype."""
+    if out is not None and out.numel() != count:
+        raise ValueError(f"{name} must hold {count} elements, has {out.numel()}")
+    return _need(out, ref.dtype, count, name, dev)
 
 
-def _norm_rope(name, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
+def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
                inv_freq, interleaved, status, stream):
-    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
-    qp, qs, T = _token_rows(q, H * G, kv, "q")
-    kp, ks, _ = _token_rows(k, H, kv, "k", T)
-    vp, vs, _ = _token_rows(v, H, kv, "v", T)
-    if q_out.dtype != kv.dtype or q_out.numel() != T * H * G * D:
-        raise ValueError(f"q_out must hold {T} tokens of {H * G} x {D} {kv.dtype}")
-    dt = str(kv.dtype).replace("torch.", "")
+    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2])
+    dev, s = _place(kv, stream)
+    i32 = torch.int32
+    qp, qs, T = _token_rows(q, H * G, kv, D, "q", dev)
+    kp, ks, _ = _token_rows(k, H, kv, D, "k", dev, T)
+    vp, vs, _ = _token_rows(v, H, kv, D, "v", dev, T)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    paged = name.endswith("_paged")
-    if paged:
-        table, B, max_pages = _block_table(where)
-        place = [table, max_pages]
-    else:
-        B, place = planes, [_arg(where, "int32", 1, "end_col")]
+    B = where.shape[0] if paged else planes
     if cu_seqlens is None and (T % B or not T):
         raise ValueError(f"{T} tokens are no whole number for each of {B} sequences")
     N = T // B if cu_seqlens is None else 0
-    sizes = [planes, H, cols, D, int(layer), T] + ([B] if paged else []) + [N, G]
+    if paged:
+        sizes = (planes, H, cols, D, int(layer), T, B, N, G, _need(where, i32, B, "block_table", dev), where.shape[1])
+    else:
+        sizes = (planes, H, cols, D, int(layer), T, N, G, _need(where, i32, 1, "end_col", dev))
     code = getattr(library(), name)(
-        qp, qs, kp, ks, vp, vs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
-        _arg(cu_seqlens, "int32", B + 1, "cu_seqlens", True), _arg(positions, "int32", T, "positions", True),
-        _arg(q_weight, dt, D, "q_weight", True), _arg(k_weight, dt, D, "k_weight", True), float(eps),
-        _arg(inv_freq, "float32", 0, "inv_freq", True) if rot else None, rot, int(bool(interleaved)), _ptr(q_out),
-        _arg(status, "int32", B, "status", True), _stream(stream))
+        qp, qs, kp, ks, vp, vs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev, True), _need(positions, i32, T, "positions", dev, True),
+        _need(q_weight, kv.dtype, D, "q_weight", dev, True), _need(k_weight, kv.dtype, D, "k_weight", dev, True),
+        eps, _need(inv_freq, torch.float32, 0, "inv_freq", dev) if rot else None, rot, 1 if interleaved else 0,
+        _same_size(q_out, kv, T * H * G * D, "q_out", dev), _need(status, i32, B, "status", dev, True), s)
     _check(code, name)
 
 
@@ -446,41 +478,34 @@ def spec_norm_rope_kv(q, k, v, kv, layer: int, end_col, kv_len, q_out, *, cu_seq
     """q [..., H * G, D], k, v [..., H, D] (views of a fused projection will do), kv [L, 2, B, H, C, D]:
     norms and rotates queries (to q_out) and keys, and writes keys and values into the cache slots.
     Without cu_seqlens B sequences of N tokens at columns E .. E + N - 1; with it packed prompts."""
-    _norm_rope("spec_norm_rope_kv", q, k, v, kv, layer, end_col, kv_len, q_out, cu_seqlens, positions, q_weight,
-               k_weight, eps, inv_freq, interleaved, status, stream)
+    _norm_rope("spec_norm_rope_kv", False, q, k, v, kv, layer, end_col, kv_len, q_out, cu_seqlens, positions,
+               q_weight, k_weight, eps, inv_freq, interleaved, status, stream)
 
 
 def spec_norm_rope_kv_paged(q, k, v, pool, layer: int, block_table, kv_len, q_out, *, cu_seqlens=None,
                             positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
                             interleaved: bool = False, status=None, stream=None) -> None:
     """spec_norm_rope_kv into a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages] int32."""
-    _norm_rope("spec_norm_rope_kv_paged", q, k, v, pool, layer, block_table, kv_len, q_out, cu_seqlens, positions,
-               q_weight, k_weight, eps, inv_freq, interleaved, status, stream)
+    _norm_rope("spec_norm_rope_kv_paged", True, q, k, v, pool, layer, block_table, kv_len, q_out, cu_seqlens,
+               positions, q_weight, k_weight, eps, inv_freq, interleaved, status, stream)
 
 
-def _out_rows(out, q, name: str = "out"):
-    if out.dtype != q.dtype or out.numel() != q.numel():
-        raise ValueError(f"{name} must match {tuple(q.shape)} {q.dtype}, got {tuple(out.shape)} {out.dtype}")
-    return _ptr(out)
-
-
-def _scale(scale, D: int) -> float:
-    return float(D) ** -0.5 if scale is None else float(scale)
-
-
-def _prompt(name, q, kv, layer, cu_seqlens, where, kv_len, out, scale, lse, status, stream):
-    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
-    qp, qs, T = _token_rows(q, H * G, kv, "q")
-    if name.endswith("_paged"):
-        table, B, max_pages = _block_table(where)
-        sizes, place = [planes, H, cols, D, int(layer), B, T, G], [table, max_pages]
+def _prompt(name, paged, q, kv, layer, cu_seqlens, where, kv_len, out, scale, lse, status, stream):
+    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2])
+    dev, s = _place(kv, stream)
+    i32 = torch.int32
+    qp, qs, T = _token_rows(q, H * G, kv, D, "q", dev)
+    if paged:
+        B = where.shape[0]
+        sizes = (planes, H, cols, D, int(layer), B, T, G, _need(where, i32, B, "block_table", dev), where.shape[1])
     else:
         B = planes
-        sizes, place = [B, H, cols, D, int(layer), T, G], [_arg(where, "int32", 1, "end_col")]
+        sizes = (B, H, cols, D, int(layer), T, G, _need(where, i32, 1, "end_col", dev))
     code = getattr(library(), name)(
-        qp, qs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
-        _arg(cu_seqlens, "int32", B + 1, "cu_seqlens"), _scale(scale, D), _out_rows(out, q),
-        _arg(lse, "float32", T * H * G, "lse", True), _arg(status, "int32", B, "status", True), _stream(stream))
+        qp, qs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev), D ** -0.5 if scale is None else scale,
+        _same_size(out, kv, T * H * G * D, "out", dev), _need(lse, torch.float32, T * H * G, "lse", dev, True),
+        _need(status, i32, B, "status", dev, True), s)
     _check(code, name)
 
 
@@ -488,14 +513,14 @@ def spec_prompt_attention(q, kv, layer: int, cu_seqlens, end_col, kv_len, out, *
                           stream=None) -> None:
     """Causal attention of packed prompts q [T, H * G, D] over the cache kv [L, 2, B, H, C, D] that holds
     their rows; out [T, H * G, D].  scale: 1 / sqrt(D) if None."""
-    _prompt("spec_prompt_attention", q, kv, layer, cu_seqlens, end_col, kv_len, out, scale, lse, status, stream)
+    _prompt("spec_prompt_attention", False, q, kv, layer, cu_seqlens, end_col, kv_len, out, scale, lse, status, stream)
 
 
 def spec_prompt_attention_paged(q, pool, layer: int, cu_seqlens, block_table, kv_len, out, *, scale=None, lse=None,
                                 status=None, stream=None) -> None:
     """spec_prompt_attention over a page pool [L, 2, pages, H, page_size, D]."""
-    _prompt("spec_prompt_attention_paged", q, pool, layer, cu_seqlens, block_table, kv_len, out, scale, lse, status,
-            stream)
+    _prompt("spec_prompt_attention_paged", True, q, pool, layer, cu_seqlens, block_table, kv_len, out, scale, lse,
+            status, stream)
 
 
 def spec_tree_attention_workspace_bytes(B: int, N: int, H: int, G: int, D: int, max_rows: int,
@@ -504,24 +529,26 @@ def spec_tree_attention_workspace_bytes(B: int, N: int, H: int, G: int, D: int, 
     return int(library().spec_tree_attention_workspace_bytes(B, N, H, G, D, max_rows, dtype_code))
 
 
-def _tree(name, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, status, stream):
+def _tree(name, paged, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, status, stream):
     if q.dim() != 4:
         raise ValueError(f"q must be [B, N, heads, D], got {tuple(q.shape)}")
-    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2], "q")
-    qp, qs, T = _token_rows(q, H * G, kv, "q")
-    B, N = q.shape[:2]
-    if name.endswith("_paged"):
-        table, rows, max_pages = _block_table(where)
-        sizes, place = [planes, H, cols, D, int(layer), B, N, G], [table, max_pages]
+    B, N, heads, _ = q.shape
+    L, planes, H, cols, D, G = _cache_dims(kv, heads)
+    dev, s = _place(kv, stream)
+    i32 = torch.int32
+    qp, qs, T = _token_rows(q, heads, kv, D, "q", dev)
+    if (where.shape[0] if paged else planes) != B:
+        raise ValueError(f"q has {B} sequences, the cache {where.shape[0] if paged else planes}")
+    if paged:
+        sizes = (planes, H, cols, D, int(layer), B, N, G, _need(where, i32, B, "block_table", dev), where.shape[1])
     else:
-        rows, sizes, place = planes, [planes, H, cols, D, int(layer), N, G], [_arg(where, "int32", 1, "end_col")]
-    if rows != B:
-        raise ValueError(f"q has {B} sequences, the cache {rows}")
+        sizes = (B, H, cols, D, int(layer), N, G, _need(where, i32, 1, "end_col", dev))
     code = getattr(library(), name)(
-        qp, qs, _ptr(kv), _dtype_code(kv), L, *sizes, *place, _arg(kv_len, "int32", B, "kv_len"),
-        _arg(mask, "int32", B * N * ((N + 31) // 32), "mask", True), _scale(scale, D), _out_rows(out, q),
-        _arg(lse, "float32", T * H * G, "lse", True), _arg(status, "int32", B, "status", True),
-        None if ws is None else _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+        qp, qs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        _need(mask, i32, T * ((N + 31) // 32), "mask", dev, True), D ** -0.5 if scale is None else scale,
+        _same_size(out, kv, T * heads * D, "out", dev), _need(lse, torch.float32, T * heads, "lse", dev, True),
+        _need(status, i32, B, "status", dev, True), None if ws is None else _need(ws, ws.dtype, 0, "ws", dev),
+        0 if ws is None else ws.numel() * ws.element_size(), s)
     _check(code, name)
 
 
@@ -530,10 +557,11 @@ def spec_tree_attention(q, kv, layer: int, end_col, kv_len, out, ws=None, *, mas
     """Attention of q [B, N, H * G, D] (the verify forward's nodes, their slots already at columns
     E .. E + N - 1 of kv [L, 2, B, H, C, D]) over the cached rows and each node's visible nodes;
     mask [B, N, ceil(N / 32)] int32 as from spec_tree_mask, None: a chain.  out [B, N, H * G, D]."""
-    _tree("spec_tree_attention", q, kv, layer, end_col, kv_len, out, ws, mask, scale, lse, status, stream)
+    _tree("spec_tree_attention", False, q, kv, layer, end_col, kv_len, out, ws, mask, scale, lse, status, stream)
 
 
 def spec_tree_attention_paged(q, pool, layer: int, block_table, kv_len, out, ws=None, *, mask=None, scale=None,
                               lse=None, status=None, stream=None) -> None:
     """spec_tree_attention over a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages]."""
-    _tree("spec_tree_attention_paged", q, pool, layer, block_table, kv_len, out, ws, mask, scale, lse, status, stream)
+    _tree("spec_tree_attention_paged", True, q, pool, layer, block_table, kv_len, out, ws, mask, scale, lse, status,
+          stream)

@@ -141,11 +141,38 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         sv.spec_tree_attention(torch.zeros(2, 3, 3, 64), kv, 0, None, None, q, None)
     with pytest.raises(ValueError, match="must be on the GPU"):
         sv.spec_tree_attention(q, kv, 0, None, None, q, None)
-    with pytest.raises(ValueError, match="must be torch.float32"):
-        sv.spec_tree_attention(q.bfloat16(), kv, 0, None, None, q, None)
     with pytest.raises(ValueError, match=r"\[B, N, heads, D\]"):
         sv.spec_tree_attention(q[0], kv, 0, None, None, q, None)
     with pytest.raises(ValueError, match=r"\[L, 2, planes, H, cols, D\]"):
         sv.spec_prompt_attention(q[0], kv[0], 0, None, None, None, q)
-    with pytest.raises(ValueError, match="must be"):
-        sv.spec_norm_rope_kv(q, q[:, :, :2, :32], q[:, :, :2], kv, 0, None, None, q)
+    with pytest.raises(ValueError, match="the cache must be contiguous"):
+        sv.spec_norm_rope_kv(q, q[:, :, :2], q[:, :, :2], kv.transpose(4, 5).contiguous().transpose(4, 5), 0, None,
+                             None, q)
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        sv.spec_tree_mask(torch.zeros(1, 4, dtype=torch.int32), None, None, None, None)
+
+
+def test_binding_checks_rows():
+    """Layout checks of query rows (device -1: host tensors stand in)."""
+    kv = torch.zeros(1, 2, 2, 2, 8, 64)
+    wide = torch.zeros(2, 3, 8, 64)
+    p, step, count = sv._token_rows(wide[:, :, :4], 4, kv, 64, "q", -1)
+    assert (step, count) == (512, 6) and p == wide.data_ptr()
+    assert sv._token_rows(wide[:, :1, :4], 4, kv, 64, "q", -1)[1:] == (1536, 2)     # one token a sequence
+    assert sv._token_rows(wide[:1, :1, :4], 4, kv, 64, "q", -1)[1:] == (256, 1)
+    for t, why in [(wide.bfloat16(), "must be torch.float32"), (wide[:, :, :3], r"must be \[\.\.\., 4, 64\]"),
+                   (wide[:, :, ::2], "contiguous"), (wide[:, :2, :4], "one stride"),
+                   (wide.transpose(2, 3)[:, :, :4, :].expand(2, 3, 4, 8), "must be")]:
+        with pytest.raises(ValueError, match=why):
+            sv._token_rows(t, 4, kv, 64, "q", -1)
+    with pytest.raises(ValueError, match="needs 5 tokens, has 6"):
+        sv._token_rows(wide[:, :, :4], 4, kv, 64, "k", -1, 5)
+    t = torch.zeros(8, dtype=torch.int32)
+    assert sv._need(None, torch.int32, 1, "mask", -1, True) is None
+    for args, why in [((None, torch.int32, 1, "kv_len", -1), "kv_len is required"),
+                      ((t, torch.int64, 1, "kv_len", -1), "must be torch.int64"),
+                      ((t, torch.int32, 9, "kv_len", -1), "at least 9 elements"),
+                      ((t, torch.int32, 8, "kv_len", 0), "must be on cuda:0"),
+                      ((t[::2], torch.int32, 4, "kv_len", -1), "must be contiguous")]:
+        with pytest.raises(ValueError, match=why):
+            sv._need(*args)

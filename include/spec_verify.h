@@ -628,11 +628,12 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *   out          [B, N, H * G, D] out; lse [B, N, H * G] out or NULL
  *   ws           workspace of spec_tree_attention_workspace_bytes(B, N, H, G,
  *                D, max_rows, dt), max_rows = C, or max_pages * page_size
- *                (contents ignored on entry; NULL if the query is 0)
+ *                (contents ignored on entry)
  * A row that sees nothing, or only scores of -inf, gives zeros and an lse of
  * -inf.  Rows that are not seen may hold anything, infinities and NaNs too.
- * Results do not depend on the other sequences' values and are the same in
- * every call.
+ * Results are the same in every call.  The cache rows are cut over workgroups
+ * by the lengths of the whole batch, so a sequence's result may differ by
+ * rounding between batches of other lengths.
  * Errors of these calls: SPEC_EINVAL for NULL required pointers, sizes < 1,
  * layer outside [0, L), strides or addresses that are not multiples of 16
  * bytes, scale or eps out of range, outputs that overlap inputs or each other,

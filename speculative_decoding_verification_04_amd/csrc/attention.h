@@ -47,10 +47,11 @@ struct Params {
   int N, words;               // trees: nodes per sequence, mask words per node
   const uint32_t *mask;       // trees: [B][N][words], or NULL: a chain
   float scale, sl;            // sl = scale * log2(e)
-  int splits, row_tiles;      // trees
-  float *part_o;              // [slot][32 * RW][D], slot = ((b * H + h) * row_tiles + rt) * splits + s
-  float *part_ml;             // [slot][32 * RW][2]: maximum (of q.k) and sum
-  int32_t *part_bad;          // [slot]: status bits found on the way
+  int target, row_tiles;      // trees: pieces aimed at; row tiles per (sequence, KV head)
+  int32_t *pieces;            // [group][2]: first slot and number of pieces
+  float *part_o;              // [slot][32 * RW][D] partial outputs
+  float2 *part_ml;            // [slot][32 * RW] maximum (of q.k) and sum
+  int32_t *part_bad;          // [slot] whether a bad page was met
 };
 
 // What a workgroup works on: rows [0, R) are (token, group head) pairs of
@@ -77,8 +78,9 @@ struct Shape {
   static constexpr int kLoads = kKT * kChunks / kThreads; // chunks of K (or V) that a lane brings
   static constexpr int kTile = kKT * DP * kElt;           // bytes of K (or V)
   static constexpr int kLds = 2 * kTile;                  // of one buffer
-  static constexpr int kJoin = (kKW - 1) * RW * 32 * DP * 4;
-  static_assert(kLoads * kThreads == kKT * kChunks && kJoin <= kLds && 2 * kLds <= 160 * 1024 - 2048, "LDS");
+  static constexpr int kJoin = RW * 32 * DP * 4;          // outputs of the RW waves side by side
+  static constexpr int kJoins = kLds / kJoin;             // that many in a buffer
+  static_assert(kLoads * kThreads == kKT * kChunks && (kKW == 1 || 2 * kJoins >= kKW) && 2 * kLds <= 160 * 1024 - 2048, "LDS");
 };
 
 // LDS place of chunk c of row r.  Rows of 256 bytes and more all start at bank
@@ -118,6 +120,14 @@ __device__ inline bf16x4b read_turned(const char *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds) const_cast<char *>(p));
 }
 
+// A value that the compiler takes for new: what is computed from it stays where
+// it is used.  Two dozen LDS addresses kept across a loop instead cost more
+// registers than a wave has beside its tiles, and an xor each is free.
+__device__ inline int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The state of one wave's 32 query rows.
 template <typename T, int DP>
 struct Rows {
@@ -125,8 +135,17 @@ struct Rows {
   typedef typename std::conditional<sizeof(T) == 2, bf16x8, f32x4>::type QV;
   QV q[kQ];
   f32x16 o[DP / 32];
-  float m, l;                 // maximum of q.k so far; this half's sum
-  uint32_t sees;              // trees: any bit of the row's mask
+  float m, l;                 // maximum of q.k so far; this half's sum (the whole sum after walk())
+};
+
+// What a wave holds of its rows once the walk is over: with KW waves on the same
+// rows the kw-th DP / KW elements, d = 8 (kw DP / 8 / KW + i) + 4 hf .. + 3.
+template <int DP, int KW>
+struct Done {
+  f32x4 o[DP / 8 / KW];
+  float m, l;
+  int token, head, kw;
+  bool mine;
 };
 
 // Brings K and V tiles from the cache straight into LDS.  A wave's load writes
@@ -227,14 +246,6 @@ __device__ inline uint32_t seen(const Params &P, const Job &J, int token, int k0
   const int left = J.total - k0;                          // bits past the tree's end
   const uint32_t valid = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
   return (bits | cached) & valid;
-}
-
-// A value that the compiler takes for new: what is computed from it stays in
-// the loop.  Two dozen LDS addresses kept across the loop instead cost more
-// registers than the wave has beside its tiles, and an xor each is free.
-__device__ inline int fresh(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
 }
 
 // One tile: the wave's scores, the softmax step and the second product.
@@ -341,7 +352,7 @@ template <typename T, int DP, int RW, bool PAGED>
 __device__ inline void add_odd(const Params &P, const Job &J, Rows<T, DP> &W, int k0,
                                const uint32_t (&vis)[Shape<T, DP, RW>::kNB]) {
   using S = Shape<T, DP, RW>;
-  const int hf = (threadIdx.x & (kWave - 1)) >> 5;
+  const int hf = fresh(threadIdx.x & (kWave - 1)) >> 5;
   for (int j = 0; j < 32 * S::kNB; ++j) {
     const int r = k0 + j;
     if (r >= J.total) break;
@@ -380,16 +391,21 @@ __device__ inline void put4(char *out, int d0, int D, const float (&x)[4]) {
   }
 }
 
-// The whole walk of one job.  slot < 0: outputs are final; else partials.
+// The walk of one job.  The waves kw == 0 return with their rows' unscaled
+// outputs, maxima and sums; all return whether a bad page was met.
 template <typename T, int DP, int RW, bool PAGED, bool PROMPT>
-__device__ inline int walk(const Params &P, const Job &J, long long slot, char *buf0, char *buf1) {
+__device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP, RW>::kKW> &D, char *buf0,
+                            char *buf1) {
   using S = Shape<T, DP, RW>;
-  const int lane = threadIdx.x & (kWave - 1), n = lane & 31, hf = lane >> 5;
-  const int wave = threadIdx.x / kWave, rw = wave % RW, kw = wave / RW;
+  const int lane = fresh(threadIdx.x & (kWave - 1)), n = lane & 31, hf = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rw = wave % RW, kw = wave / RW;
   const int R = J.tokens * P.G;
   const int row = min(J.row0 + rw * 32 + n, R - 1);       // rows past the end repeat the last
-  const bool mine = J.row0 + rw * 32 + n < R;
   const int token = row / P.G, head = J.h * P.G + (row - token * P.G);
+  D.mine = J.row0 + rw * 32 + n < R;
+  D.token = token;
+  D.head = head;
+  D.kw = kw;
   Rows<T, DP> W;
   {
     const char *q = P.q + (J.token0 + token) * P.q_stride + static_cast<long long>(head) * P.c.D * S::kElt;
@@ -406,12 +422,6 @@ __device__ inline int walk(const Params &P, const Job &J, long long slot, char *
     for (int r = 0; r < 16; ++r) W.o[db][r] = 0.0f;
   W.m = -INFINITY;
   W.l = 0.0f;
-  W.sees = 1;
-  if (!PROMPT && P.mask) {
-    W.sees = 0;
-    for (int i = 0; i < P.words; ++i)
-      W.sees |= P.mask[(static_cast<long long>(J.b) * P.N + token) * P.words + i];
-  }
   // cache rows below `plain` are seen by every row of the workgroup
   const int plain = !PROMPT && P.mask ? J.limit0 - 1 : J.limit0 + J.row0 / P.G;
   Loader<T, DP, RW, PAGED> ld(P, J);
@@ -462,86 +472,82 @@ __device__ inline int walk(const Params &P, const Job &J, long long slot, char *
     now = next;
     next = x;
   }
-  float l = half_sum(W.l), m = W.m;
-  // Join the waves that shared the rows: each brings its maximum, sum and
-  // output; the first adds them, scaled to the common maximum.
+  W.l = half_sum(W.l);
   if constexpr (S::kKW > 1) {
+    // Join the waves that shared the rows.  Each leaves its outputs in LDS, four
+    // values of a row side by side, and takes its share of the row's elements
+    // from all of them, scaled to the common maximum.
+    __syncthreads();                                      // the tiles are read
+    __shared__ float2 jm[4][32];
+    auto place_of = [&](int k) {                          // [rw][DP / 4][32] of the k-th wave behind each other
+      char *buf = k < S::kJoins ? buf0 + k * S::kJoin : buf1 + (k - S::kJoins) * S::kJoin;
+      return reinterpret_cast<f32x4 *>(buf) + rw * (DP / 4 * 32) + hf * 32 + n;
+    };
+    f32x4 *mine = place_of(kw);
+#pragma unroll
+    for (int q = 0; q < DP / 8; ++q)                      // q = 4 db + g: d = 8 q + 4 hf ..
+      mine[q * 64] = f32x4{W.o[q / 4][4 * (q % 4)], W.o[q / 4][4 * (q % 4) + 1], W.o[q / 4][4 * (q % 4) + 2],
+                           W.o[q / 4][4 * (q % 4) + 3]};
+    if (hf == 0) jm[wave][n] = make_float2(W.m, W.l);
     __syncthreads();
-    float *jo = reinterpret_cast<float *>(buf0);          // [kw - 1][rw][DP][32]
-    __shared__ float jm[(S::kKW - 1) * RW * 64];          // [kw - 1][rw][2][32]
-    if (kw > 0) {
-      float *o = jo + ((kw - 1) * RW + rw) * 32 * DP;
+    float2 ml[S::kKW];
+    float top = -INFINITY;
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[(32 * db + 8 * (r / 4) + 4 * hf + r % 4) * 32 + n] = W.o[db][r];
-      if (hf == 0) {
-        float *x = jm + ((kw - 1) * RW + rw) * 64;
-        x[n] = m;
-        x[32 + n] = l;
-      }
+    for (int k = 0; k < S::kKW; ++k) {
+      ml[k] = jm[k * RW + rw][n];
+      top = fmaxf(top, ml[k].x);
     }
-    __syncthreads();
-    if (kw == 0) {
-      float top = m;
+    const float base = top == -INFINITY ? 0.0f : top;
+    D.m = top;
+    D.l = 0.0f;
+    constexpr int kMine = DP / 8 / S::kKW;                // quads of this wave
 #pragma unroll
-      for (int k = 0; k < S::kKW - 1; ++k) top = fmaxf(top, jm[(k * RW + rw) * 64 + n]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      const float a = __builtin_amdgcn_exp2f((m - base) * P.sl);
-      l *= a;
+    for (int i = 0; i < kMine; ++i) D.o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db)
+    for (int k = 0; k < S::kKW; ++k) {
+      const float f = __builtin_amdgcn_exp2f((ml[k].x - base) * P.sl);
+      D.l = fmaf(ml[k].y, f, D.l);
+      const f32x4 *o = place_of(k) + kw * kMine * 64;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) W.o[db][r] *= a;
-      for (int k = 0; k < S::kKW - 1; ++k) {
-        const float *x = jm + (k * RW + rw) * 64;
-        const float *o = jo + (k * RW + rw) * 32 * DP;
-        const float f = __builtin_amdgcn_exp2f((x[n] - base) * P.sl);
-        l = fmaf(x[32 + n], f, l);
-#pragma unroll
-        for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            W.o[db][r] = fmaf(o[(32 * db + 8 * (r / 4) + 4 * hf + r % 4) * 32 + n], f, W.o[db][r]);
-      }
-      m = top;
+      for (int i = 0; i < kMine; ++i) D.o[i] += o[i * 64] * f;
     }
+  } else {
+    D.m = W.m;
+    D.l = W.l;
+#pragma unroll
+    for (int q = 0; q < DP / 8; ++q)
+      D.o[q] = f32x4{W.o[q / 4][4 * (q % 4)], W.o[q / 4][4 * (q % 4) + 1], W.o[q / 4][4 * (q % 4) + 2],
+                        W.o[q / 4][4 * (q % 4) + 3]};
   }
-  if (kw == 0 && mine) {
-    const int D = P.c.D;
-    if (slot >= 0) {
-      float *o = P.part_o + (slot * (32 * RW) + rw * 32 + n) * D;
+  return PAGED && __syncthreads_or(ld.bad);
+}
+
+// Trees: whether a node's mask row has any bit (else it sees nothing at all).
+__device__ inline bool sees_any(const Params &P, int b, int token) {
+  if (!P.mask) return true;
+  uint32_t any = 0;
+  for (int i = 0; i < P.words; ++i) any |= P.mask[(static_cast<long long>(b) * P.N + token) * P.words + i];
+  return any != 0;
+}
+
+// Final results of a wave's rows.  A row that saw nothing has sum 0 (its
+// maximum is -inf): zeros.
+template <typename T, int DP, int KW>
+__device__ inline void put_rows(const Params &P, const Job &J, const Done<DP, KW> &D, bool sees) {
+  const int hf = fresh(threadIdx.x & (kWave - 1)) >> 5;
+  if (!D.mine) return;
+  const bool none = !sees || D.l == 0.0f;
+  const float f = none ? 0.0f : 1.0f / D.l;
+  const long long at = (J.token0 + D.token) * P.c.H * P.G + D.head;
+  char *o = P.out + at * P.c.D * sizeof(T);
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db)
+  for (int i = 0; i < DP / 8 / KW; ++i) {
+    float x[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float x[4] = {W.o[db][4 * g], W.o[db][4 * g + 1], W.o[db][4 * g + 2], W.o[db][4 * g + 3]};
-          put4<float>(reinterpret_cast<char *>(o), 32 * db + 8 * g + 4 * hf, D, x);
-        }
-      if (hf == 0) {
-        float *x = P.part_ml + (slot * (32 * RW) + rw * 32 + n) * 2;
-        x[0] = m;
-        x[1] = l;
-      }
-    } else {
-      // a row that saw nothing has sum 0 (its maximum is -inf): zeros
-      const bool none = W.sees == 0 || l == 0.0f;
-      const float f = none ? 0.0f : 1.0f / l;
-      const long long at = (J.token0 + token) * P.c.H * P.G + head;
-      char *o = P.out + at * D * S::kElt;
-#pragma unroll
-      for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float x[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = none ? 0.0f : W.o[db][4 * g + j] * f;
-          put4<T>(o, 32 * db + 8 * g + 4 * hf, D, x);
-        }
-      if (P.lse && hf == 0) P.lse[at] = none ? -INFINITY : m * P.scale + logf(l);
-    }
+    for (int j = 0; j < 4; ++j) x[j] = none ? 0.0f : D.o[i][j] * f;
+    put4<T>(o, 8 * (D.kw * (DP / 8 / KW) + i) + 4 * hf, P.c.D, x);
   }
-  return PAGED && __syncthreads_or(ld.bad) ? SPEC_ST_BAD_STATE : 0;
+  if (P.lse && hf == 0 && D.kw == 0) P.lse[at] = none ? -INFINITY : D.m * P.scale + logf(D.l);
 }
 
 // Zeros for the rows of a job whose sequence's state is out of range.
@@ -585,9 +591,10 @@ inline int fill(Params &P, const void *q, int64_t q_stride, const void *kv, spec
   P.mask = nullptr;
   P.scale = scale;
   P.sl = scale * 1.44269504088896340736f;
-  P.splits = P.row_tiles = 1;
-  P.part_o = P.part_ml = nullptr;
-  P.part_bad = nullptr;
+  P.target = P.row_tiles = 1;
+  P.part_o = nullptr;
+  P.part_ml = nullptr;
+  P.part_bad = P.pieces = nullptr;
   return SPEC_OK;
 }
 

@@ -13,16 +13,20 @@
 //
 // Design.  Bound by HBM: each element is read once and written once.  One
 // workgroup per token; a group of lanes takes one head, 16 bytes a lane, and
-// keeps its cosines and sines in registers over the heads that it takes, so a
-// token's angles are computed once for all its heads.  A lane reads its
-// partners' chunk itself (a second load of the same head, from the cache)
-// rather than exchanging eight values with another lane.
+// every lane issues the loads of all its heads before anything else.  The
+// token's cosines and sines are computed once, by one lane each, and shared
+// through LDS with the weights.  A lane reads its partners' chunk itself (a
+// second load of the same head, from the cache) rather than exchanging eight
+// values with another lane.
 #include "cache_view.h"
 
 namespace specv {
 namespace {
 
 constexpr int kMaxThreads = 256;
+constexpr int kU = 4;      // heads in flight per lane
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct RopeParams {
   CacheView c;
@@ -42,20 +46,20 @@ template <> struct Vec<float> { static constexpr int n = 4; };
 template <> struct Vec<__bf16> { static constexpr int n = 8; };
 
 template <typename T>
-__device__ inline void load_chunk(const void *p, float (&x)[Vec<T>::n]) {
+__device__ inline void widen(u32x4 p, float (&x)[Vec<T>::n]) {
   typedef T V __attribute__((ext_vector_type(Vec<T>::n)));
-  const V v = *static_cast<const V *>(p);
+  const V v = __builtin_bit_cast(V, p);
 #pragma unroll
   for (int j = 0; j < Vec<T>::n; ++j) x[j] = static_cast<float>(v[j]);
 }
 
 template <typename T>
-__device__ inline void store_chunk(void *p, const float (&x)[Vec<T>::n]) {
+__device__ inline u32x4 narrow(const float (&x)[Vec<T>::n]) {
   typedef T V __attribute__((ext_vector_type(Vec<T>::n)));
   V v;
 #pragma unroll
   for (int j = 0; j < Vec<T>::n; ++j) v[j] = static_cast<T>(x[j]);
-  *static_cast<V *>(p) = v;
+  return __builtin_bit_cast(u32x4, v);
 }
 
 // A sequence's new tokens and where their rows start.
@@ -112,12 +116,55 @@ __device__ inline void write_status(const RopeParams &P, int b) {
 template <typename T>
 __global__ __launch_bounds__(kMaxThreads) void norm_rope_kernel(RopeParams P) {
   constexpr int kN = Vec<T>::n;
+  __shared__ float2 angle[SPEC_ATTN_MAX_D / 2];
+  __shared__ float weight[2][SPEC_ATTN_MAX_D];
   const int lane = threadIdx.x & (kWave - 1);
   if (blockIdx.x >= static_cast<unsigned>(P.T)) {
     write_status(P, (blockIdx.x - P.T) * (blockDim.x / kWave) + threadIdx.x / kWave);
     return;
   }
   const int t = blockIdx.x;
+  const int D = P.c.D, half = P.half;
+  const int lph = P.lanes, g = threadIdx.x / lph, e0 = (threadIdx.x & (lph - 1)) * kN;
+  const bool active = e0 < D;
+  const int heads = P.Hq + 2 * P.c.H, step = blockDim.x / lph;
+  // Element e turns with mate(e): e ^ 1, or e + half, or e - half.
+  auto mate = [&](int e) {
+    e = min(e, D - 1);
+    if (e >= 2 * half) return e;
+    return P.interleaved ? e ^ 1 : e < half ? e + half : e - half;
+  };
+  const bool whole = half % kN == 0;                      // a chunk's partners are one chunk
+  u32x4 x[kU], y[kU];
+  auto fetch = [&](int h0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int h = h0 + u * step;
+      x[u] = y[u] = u32x4{0, 0, 0, 0};
+      if (h >= heads || !active) continue;
+      const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.c.H;
+      const int hh = is_q ? h : is_k ? h - P.Hq : h - P.Hq - P.c.H;
+      const char *src = (is_q ? P.q + t * P.q_stride : is_k ? P.k + t * P.k_stride : P.v + t * P.v_stride) +
+                        static_cast<long long>(hh) * D * sizeof(T);
+      x[u] = *reinterpret_cast<const u32x4 *>(src + e0 * sizeof(T));
+      if ((is_q || is_k) && !P.interleaved) {
+        if (whole) {
+          y[u] = *reinterpret_cast<const u32x4 *>(src + mate(e0) * sizeof(T));
+        } else {
+          typedef T V __attribute__((ext_vector_type(kN)));
+          V v;
+#pragma unroll
+          for (int j = 0; j < kN; ++j) v[j] = reinterpret_cast<const T *>(src)[mate(e0 + j)];
+          y[u] = __builtin_bit_cast(u32x4, v);
+        }
+      }
+    }
+  };
+  fetch(g);
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    weight[0][i] = P.q_weight ? static_cast<float>(static_cast<const T *>(P.q_weight)[i]) : 1.0f;
+    weight[1][i] = P.k_weight ? static_cast<float>(static_cast<const T *>(P.k_weight)[i]) : 1.0f;
+  }
   int b = -1;
   if (P.cu) {
     // the first sequence that holds token t
@@ -151,78 +198,67 @@ __global__ __launch_bounds__(kMaxThreads) void norm_rope_kernel(RopeParams P) {
     slot = cache_offset(P.c, write ? plane : 0, 0, col, sizeof(T));
   }
   const long long head_step = static_cast<long long>(P.c.cols) * P.c.D * sizeof(T);
-  const int D = P.c.D, half = P.half;
-  const int lph = P.lanes, g = threadIdx.x / lph, e0 = (threadIdx.x & (lph - 1)) * kN;
-  const bool active = e0 < D;
   const int pos = P.positions ? P.positions[t] : row;
-  // This lane's angles and partners: element e's partner is e ^ 1, or
-  // e + half, or e - half; c = cos, sn = sin with the sign that its side takes.
-  float c[kN], sn[kN];
-  int mate[kN];
+  for (int i = threadIdx.x; i < half; i += blockDim.x) {
+    const double turn = static_cast<double>(pos) * P.inv_freq[i] * 0.15915494309189533577;
+    float sv, cv;
+    sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sv, &cv);
+    angle[i] = make_float2(cv, sv);
+  }
+  __syncthreads();
+  float c[kN], sn[kN];                                    // sn: the sine with the sign that the element's side takes
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    const int e = e0 + j;
+    const int e = min(e0 + j, D - 1);
     c[j] = 1.0f;
     sn[j] = 0.0f;
-    mate[j] = min(e, D - 1);
-    if (active && e < 2 * half) {
-      const int i = P.interleaved ? e >> 1 : (e < half ? e : e - half);
-      const bool low = P.interleaved ? !(e & 1) : e < half;
-      const double turn = static_cast<double>(pos) * P.inv_freq[i] * 0.15915494309189533577;
-      float sv, cv;
-      sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sv, &cv);
-      c[j] = cv;
-      sn[j] = low ? -sv : sv;
-      mate[j] = P.interleaved ? e ^ 1 : (low ? e + half : e - half);
+    if (e < 2 * half) {
+      const float2 a = angle[P.interleaved ? e >> 1 : e < half ? e : e - half];
+      c[j] = a.x;
+      sn[j] = (P.interleaved ? !(e & 1) : e < half) ? -a.y : a.y;
     }
   }
-  const bool whole = half % kN == 0;                      // a chunk's partners are one chunk
-  const int heads = P.Hq + 2 * P.c.H, step = blockDim.x / lph;
-  for (int h = g; h < heads; h += step) {
-    const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.c.H;
-    const int hh = is_q ? h : is_k ? h - P.Hq : h - P.Hq - P.c.H;
-    const char *src = (is_q ? P.q + t * P.q_stride : is_k ? P.k + t * P.k_stride : P.v + t * P.v_stride) +
-                      static_cast<long long>(hh) * D * sizeof(T);
-    float x[kN] = {};
-    if (active) load_chunk<T>(src + e0 * sizeof(T), x);
-    if (is_q || is_k) {
-      const void *wp = is_q ? P.q_weight : P.k_weight;
-      float y[kN] = {};
-      if (active) {
-        if (P.interleaved) {
+  for (int h0 = g;; h0 += kU * step) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j) y[j] = x[j ^ 1];
-        } else if (whole) {
-          if (mate[0] != e0) load_chunk<T>(src + mate[0] * sizeof(T), y);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kN; ++j) y[j] = static_cast<float>(reinterpret_cast<const T *>(src)[mate[j]]);
-        }
+    for (int u = 0; u < kU; ++u) {
+      const int h = h0 + u * step;
+      if (h >= heads) break;
+      const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.c.H;
+      const int hh = is_q ? h : is_k ? h - P.Hq : h - P.Hq - P.c.H;
+      char *to = is_q ? P.q_out + (static_cast<long long>(t) * P.Hq + hh) * D * sizeof(T) + e0 * sizeof(T)
+                      : (is_k ? P.c.k : P.c.v) + slot + hh * head_step + e0 * sizeof(T);
+      const bool store = active && (is_q || write);
+      if (!is_q && !is_k) {
+        if (store) *reinterpret_cast<u32x4 *>(to) = x[u];
+        continue;
       }
-      if (wp) {                                           // uniform over the lanes of a head
+      float a[kN], m[kN];
+      widen<T>(x[u], a);
+      if (P.interleaved) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) m[j] = a[j ^ 1];
+      } else {
+        widen<T>(y[u], m);
+      }
+      if (is_q ? P.q_weight : P.k_weight) {               // the same for a head's lanes
         float ss = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kN; ++j) ss = fmaf(x[j], x[j], ss);
+        for (int j = 0; j < kN; ++j) ss = fmaf(a[j], a[j], ss);
         for (int d = lph >> 1; d; d >>= 1) ss += __shfl_xor(ss, d);
         const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + P.eps);
-        const T *w = static_cast<const T *>(wp);
-        if (active) {
+        const float *w = weight[is_q ? 0 : 1];
 #pragma unroll
-          for (int j = 0; j < kN; ++j) {
-            x[j] = x[j] * r * static_cast<float>(w[e0 + j]);
-            y[j] = y[j] * r * static_cast<float>(w[mate[j]]);
-          }
+        for (int j = 0; j < kN; ++j) {
+          a[j] = a[j] * r * w[min(e0 + j, D - 1)];
+          m[j] = m[j] * r * w[mate(e0 + j)];
         }
       }
 #pragma unroll
-      for (int j = 0; j < kN; ++j) x[j] = e0 + j < 2 * half ? fmaf(y[j], sn[j], x[j] * c[j]) : x[j];
+      for (int j = 0; j < kN; ++j) a[j] = e0 + j < 2 * half ? fmaf(m[j], sn[j], a[j] * c[j]) : a[j];
+      if (store) *reinterpret_cast<u32x4 *>(to) = narrow<T>(a);
     }
-    if (active) {
-      if (is_q)
-        store_chunk<T>(P.q_out + (static_cast<long long>(t) * P.Hq + hh) * D * sizeof(T) + e0 * sizeof(T), x);
-      else if (write)
-        store_chunk<T>((is_k ? P.c.k : P.c.v) + slot + hh * head_step + e0 * sizeof(T), x);
-    }
+    if (h0 + kU * step >= heads) break;
+    fetch(h0 + kU * step);
   }
 }
 

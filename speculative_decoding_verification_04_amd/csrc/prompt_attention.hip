@@ -100,8 +100,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
   const int last = min((J.row0 + kTileRows - 1) / P.G, len - 1);      // the tile's last token
   J.t0 = 0;
   J.t1 = (J.limit0 + last + S::kKT - 1) / S::kKT;
-  const int bad = walk<T, DP, kRW, PAGED, true>(P, J, -1, buf0, buf1);
-  if (reports && threadIdx.x == 0) P.status[w.b] = bad;
+  Done<DP, 1> W;
+  const bool bad = walk<T, DP, kRW, PAGED, true>(P, J, W, buf0, buf1);
+  put_rows<T>(P, J, W, true);
+  if (reports && threadIdx.x == 0) P.status[w.b] = bad ? SPEC_ST_BAD_STATE : 0;
 }
 
 template <typename T, int DP>

@@ -8,146 +8,243 @@
 // Design.  Bound by HBM: each cache row is read once for the N * G query rows
 // of its KV head, which fit one workgroup's tile (32, 64 or 128 rows) unless
 // the tree and the group are large.  With one workgroup per (sequence, KV
-// head) a batch does not fill the chip, so the cache rows are split over
-// workgroups and a second launch joins their partial results in split order.
+// head, row tile) a batch does not fill the chip, so each such group's cache
+// rows are cut into pieces of about the same length, whatever the sequences'
+// lengths, which the workgroups find on the device; the pieces' partial results
+// go to the workspace and a second launch joins them, in the order of the
+// pieces, one wave for each query row.  (Joining them in the first launch, by
+// the workgroup that brings a group's last piece, took 19 us instead of 16 for
+// one token over 1100 rows, and 40 instead of 23 for five tokens of eight
+// sequences: one workgroup's loads of all pieces, past its L2, are slower than
+// a launch.)
 #include "attention.h"
 
 namespace specv {
 namespace {
 using namespace attn;
 
-// How a call is cut: waves side by side, row tiles, splits of the cache rows.
+#ifndef KMIN
+#define KMIN 1
+#endif
+inline int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// How a call is cut: waves side by side, row tiles, pieces aimed at.
 struct Plan {
-  int rw, tile_rows, row_tiles, splits;
-  long long slots;
+  int rw, kt, row_tiles, target;
+  long long groups, tiles, slots;   // tiles, slots (pieces): the most that the cache can give
 };
 
 inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_dtype dt) {
   Plan p;
   const long long R = static_cast<long long>(N) * G;
-  // two buffers of a tile fit LDS: 32 * 4 / rw cache rows of K and V (64 for bf16 and rw = 4)
-  const int least = (dt == SPEC_F32 ? 2 : 1) * (D > 128 ? 2 : 1);
+  // two buffers of 128 / rw cache rows (K and V, padded to dp) have to fit LDS
+  const int row = dp_of(D) * (dt == SPEC_BF16 ? 2 : 4), least = row <= 256 ? 1 : row <= 512 ? 2 : 4;
   p.rw = R > 64 || least == 4 ? 4 : R > 32 || least == 2 ? 2 : 1;
-  p.tile_rows = 32 * p.rw;
-  p.row_tiles = static_cast<int>((R + p.tile_rows - 1) / p.tile_rows);
-  const long long groups = static_cast<long long>(B) * H * p.row_tiles;
-  const long long tiles = (max_rows + 63) / 64;
-  long long want = (1024 + groups - 1) / groups;
-  if (want > tiles / 2) want = tiles / 2;
-  if (want > 64) want = 64;
-  p.splits = want < 1 ? 1 : static_cast<int>(want);
-  p.slots = groups * p.splits;
+  p.kt = p.rw == 4 ? (dt == SPEC_BF16 ? 64 : 32) : 128 / p.rw;
+  p.row_tiles = static_cast<int>((R + 32 * p.rw - 1) / (32 * p.rw));
+  p.groups = static_cast<long long>(B) * H * p.row_tiles;
+  p.tiles = p.groups * ((max_rows + p.kt - 1) / p.kt);
+  p.target = 256 * (p.rw == 1 ? 1 : 2);                    // what the chip's LDS holds at once
+  p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
+  if (p.slots > p.tiles) p.slots = p.tiles;
   return p;
 }
 
-inline size_t part_bytes(const Plan &p, int D) {
-  if (p.splits == 1) return 0;
-  return round_up(static_cast<size_t>(p.slots) * p.tile_rows * D * 4, 256) +
-         round_up(static_cast<size_t>(p.slots) * p.tile_rows * 8, 256) + round_up(static_cast<size_t>(p.slots) * 4, 256);
+// Workspace: a slot for each piece, and each group's pieces.
+struct Space {
+  size_t o, ml, bad, pieces, end;   // offsets
+};
+inline Space space_of(const Plan &p, int D) {
+  const size_t slots = static_cast<size_t>(p.slots), rows = slots * 32 * p.rw;
+  Space s;
+  s.o = 0;
+  s.ml = s.o + rows * D * 4;
+  s.bad = s.ml + rows * 8;
+  s.pieces = s.bad + slots * 4;
+  s.end = round_up(s.pieces + static_cast<size_t>(p.groups) * 8, 256);
+  return s;
 }
 
-// A sequence's status; 0: its rows may be read.
-__device__ inline int tree_status(const Params &P, int b) {
-  const int n = P.c.kv_len[b];
+// A sequence's status, for its length n and the rectangle's end E (pages: 0); 0:
+// its rows may be read.
+__device__ inline int tree_status(const Params &P, int n, int E) {
   int st = n < 0 ? SPEC_ST_BAD_STATE : 0;
   const long long cap = cache_capacity(P.c);
   if (P.c.table) {
     if (static_cast<long long>(n) + P.N > cap) st |= SPEC_ST_CAPACITY;
   } else {
-    const int E = *P.c.end_col;
     if (E < 0 || static_cast<long long>(E) + P.N > cap) st |= SPEC_ST_CAPACITY;
     if (n > E) st |= SPEC_ST_BAD_STATE;
   }
   return st;
 }
 
+// Tiles of a sequence's rows (0: not to be read).
+__device__ inline int tree_tiles(const Params &P, int n, int E, int kt) {
+  return tree_status(P, n, E) ? 0 : static_cast<int>((static_cast<long long>(n) + P.N + kt - 1) / kt);
+}
+
 template <typename T, int DP, int RW, bool PAGED>
-__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void tree_kernel(Params P) {
+__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2 : 1) void tree_kernel(Params P) {
   using S = Shape<T, DP, RW>;
   __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
   __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
-  const int x = blockIdx.x;                               // ((b * H + h) * row_tiles + rt) * splits + s
-  const int s = x % P.splits, y = x / P.splits, rt = y % P.row_tiles, bh = y / P.row_tiles;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rw = wave % RW;
+  const int H = P.c.H, each = H * P.row_tiles, E = PAGED ? 0 : *P.c.end_col;
+  // all tiles of the call; the first 64 sequences' stay in the lanes
+  const int n0 = lane < P.B ? P.c.kv_len[lane] : -1;
+  const int tiles0 = tree_tiles(P, n0, E, S::kKT);
+  int total = tiles0;                                     // the host has seen that it fits
+  for (int b = lane + kWave; b < P.B; b += kWave) total += tree_tiles(P, P.c.kv_len[b], E, S::kKT);
+  total = wave_reduce(total, [](int a, int c) { return a + c; }) * each;
+  // Tiles of a piece, at most: so many that the pieces fit the chip at once.  A
+  // few workgroups more than that would run alone behind all the others: 16-node
+  // trees over 32 sequences of 512 .. 4096 rows took 74 us so and 84 us without
+  // the second look, 255-node trees over 32k rows 324 and 410 us.
+  int per = max(1, (total + P.target - 1) / P.target);
+  if (P.B <= kWave && each * P.B <= P.target)
+    while (per > 1 && wave_reduce((tiles0 + per - 1) / per, [](int a, int c) { return a + c; }) * each > P.target)
+      per += (per + 15) / 16;
+  // this workgroup's sequence: the pieces are numbered in the order of sequence, head, row tile
   Job J;
-  J.b = bh / P.c.H;
-  J.h = bh - J.b * P.c.H;
-  J.row0 = rt * 32 * RW;
-  J.tokens = P.N;
-  J.token0 = static_cast<long long>(J.b) * P.N;
-  const int st = tree_status(P, J.b), n = P.c.kv_len[J.b];
-  const bool reports = P.status && J.h == 0 && rt == 0;
-  if (st) {
-    if (s == 0) {
-      put_zeros<T>(P, J, 32 * RW);
-      if (reports && threadIdx.x == 0) P.status[J.b] = st;
+  J.b = -1;
+  int tiles = 0, pieces = 0, first = 0, n = 0;            // of the sequence; its first piece's number
+  for (int b0 = 0; b0 < P.B; b0 += kWave) {
+    const int b = b0 + lane;
+    const int nb = b0 == 0 ? n0 : b < P.B ? P.c.kv_len[b] : -1;
+    const int tb = b0 == 0 ? tiles0 : tree_tiles(P, nb, E, S::kKT), pb = (tb + per - 1) / per;
+    const int upto = wave_incl_scan(pb * each);
+    const uint64_t who = __ballot(first + upto > static_cast<int>(blockIdx.x));
+    if (who) {
+      const int l = __ffsll(static_cast<unsigned long long>(who)) - 1;
+      J.b = b0 + l;
+      n = read_lane(nb, l);
+      tiles = read_lane(tb, l);
+      pieces = read_lane(pb, l);
+      first += read_lane(upto, l) - pieces * each;
+      break;
     }
-    return;
+    first += read_lane(upto, kWave - 1);
   }
-  J.limit0 = n + 1;
-  J.total = n + P.N;
-  J.start_col = PAGED ? 0 : *P.c.end_col - n;
-  const int tiles = (J.total + S::kKT - 1) / S::kKT;
-  J.t0 = static_cast<int>(static_cast<long long>(tiles) * s / P.splits);
-  J.t1 = static_cast<int>(static_cast<long long>(tiles) * (s + 1) / P.splits);
-  const int bad = walk<T, DP, RW, PAGED, false>(P, J, P.splits > 1 ? x : -1, buf0, buf1);
-  if (threadIdx.x == 0) {
-    if (P.splits > 1)
-      P.part_bad[x] = bad;
-    else if (reports)
-      P.status[J.b] = bad;
+  J.tokens = P.N;
+  if (J.b >= 0) {
+    const int off = blockIdx.x - first, g = off / pieces, i = off - g * pieces;   // g = h * row_tiles + rt
+    J.h = g / P.row_tiles;
+    J.row0 = (g - J.h * P.row_tiles) * 32 * RW;
+    J.token0 = static_cast<long long>(J.b) * P.N;
+    J.limit0 = n + 1;
+    J.total = n + P.N;
+    J.start_col = PAGED ? 0 : E - n;
+    J.t0 = static_cast<int>(static_cast<long long>(tiles) * i / pieces);
+    J.t1 = static_cast<int>(static_cast<long long>(tiles) * (i + 1) / pieces);
+    Done<DP, S::kKW> D;
+    const bool bad = walk<T, DP, RW, PAGED, false>(P, J, D, buf0, buf1);
+    if (pieces == 1) {
+      put_rows<T>(P, J, D, sees_any(P, J.b, D.token));
+      if (P.status && J.h == 0 && J.row0 == 0 && threadIdx.x == 0) P.status[J.b] = bad ? SPEC_ST_BAD_STATE : 0;
+    } else {
+      if (D.mine) {
+        const long long row = static_cast<long long>(blockIdx.x) * (32 * RW) + rw * 32 + (lane & 31);
+        char *o = reinterpret_cast<char *>(P.part_o + row * P.c.D);
+#pragma unroll
+        for (int q = 0; q < DP / 8 / S::kKW; ++q) {
+          const float x[4] = {D.o[q][0], D.o[q][1], D.o[q][2], D.o[q][3]};
+          put4<float>(o, 8 * (D.kw * (DP / 8 / S::kKW) + q) + 4 * (lane >> 5), P.c.D, x);
+        }
+        if (lane < 32 && D.kw == 0) P.part_ml[row] = make_float2(D.m, D.l);
+      }
+      if (threadIdx.x == 0) P.part_bad[blockIdx.x] = bad;
+    }
+    if (i == 0 && threadIdx.x == 0)
+      reinterpret_cast<int2 *>(P.pieces)[static_cast<long long>(J.b) * each + g] = make_int2(blockIdx.x, pieces);
+  }
+  // sequences that are not read: zeros
+  for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+    const int st = tree_status(P, P.c.kv_len[b], E);
+    if (!st) continue;
+    J.token0 = static_cast<long long>(b) * P.N;
+    J.row0 = 0;
+    for (J.h = 0; J.h < H; ++J.h) put_zeros<T>(P, J, P.N * P.G);
+    if (P.status && threadIdx.x == 0) P.status[b] = st;
+    for (int x = threadIdx.x; x < each; x += kThreads)
+      reinterpret_cast<int2 *>(P.pieces)[static_cast<long long>(b) * each + x] = make_int2(0, 0);
   }
 }
 
-// Joins the splits of one query row per wave, in split order.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void tree_join_kernel(Params P, int tile_rows) {
-  const int lane = threadIdx.x & (kWave - 1);
+// Joins the pieces of the groups that were cut, one wave for each query row,
+// in the order of the pieces.  DP / 4 lanes read a piece's row, 16 bytes each,
+// so a wave reads 256 / DP pieces at once.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void join_kernel(Params P, int tile_rows) {
+  constexpr int kLanes = DP / 4, kSide = kWave / kLanes, kAhead = 4;
+  const int lane = threadIdx.x & (kWave - 1), side = lane / kLanes, d0 = lane % kLanes * 4;
   const int R = P.N * P.G, D = P.c.D;
-  const long long x = static_cast<long long>(blockIdx.x) * (kThreads / kWave) + threadIdx.x / kWave;
-  if (x >= static_cast<long long>(P.B) * P.c.H * R) return;
-  const int row = static_cast<int>(x % R), bh = static_cast<int>(x / R), b = bh / P.c.H, h = bh - b * P.c.H;
-  if (tree_status(P, b)) return;                          // the first launch wrote its zeros
+  const int x = blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;   // (b * H + h) * R + row
+  if (x >= P.B * P.c.H * R) return;
+  const int row = x % R, bh = x / R, b = bh / P.c.H, h = bh - b * P.c.H;
+  const int rt = row / tile_rows, at_row = row - rt * tile_rows;
+  const int2 cut = reinterpret_cast<const int2 *>(P.pieces)[static_cast<long long>(bh) * P.row_tiles + rt];
+  const int pieces = cut.y;
+  if (pieces <= 1) return;
+  auto slot = [&](int i) { return static_cast<long long>(cut.x) + i; };
   const int token = row / P.G;
-  const long long slot0 = (static_cast<long long>(bh) * P.row_tiles + row / tile_rows) * P.splits;
-  const int at_row = row % tile_rows;
-  const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml);
-  float m = -INFINITY, l = 0.0f;
-  int bad = 0;
-  if (lane < P.splits) {                                  // at most 64 splits
-    const float2 v = ml[(slot0 + lane) * tile_rows + at_row];
-    m = v.x;
-    l = v.y;
-    bad = P.part_bad[slot0 + lane];
-  }
-  const float top = wave_max_dpp(m), base = top == -INFINITY ? 0.0f : top;
-  const float f = __builtin_amdgcn_exp2f((m - base) * P.sl);
-  const float sum = wave_reduce(l * f, [](float a, float c) { return a + c; });
-  bool sees = true;
-  if (P.mask) {
-    const uint32_t w = lane < P.words ? P.mask[(static_cast<long long>(b) * P.N + token) * P.words + lane] : 0u;
-    sees = __any(w != 0);
-  }
-  const bool none = !sees || sum == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / sum;
-  float o[4] = {};
-  const int d0 = lane * 4;
-  for (int s = 0; s < P.splits; ++s) {
-    const float w = __shfl(f, s);                         // every lane takes part: lane s may hold no elements
-    if (d0 < D) {
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(P.part_o + ((slot0 + s) * tile_rows + at_row) * D + d0);
+  uint32_t word = 1;
+  if (P.mask) word = lane < P.words ? P.mask[(static_cast<long long>(b) * P.N + token) * P.words + lane] : 0u;
+  // eight pieces' rows or so (DP = 128), asked for before their weights are known
+  f32x4 v[kAhead];
+  auto fetch = [&](int s, int end) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fmaf(v[j], w, o[j]);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = min(s + u * kSide + side, end - 1);
+      v[u] = d0 < D ? *reinterpret_cast<const f32x4 *>(P.part_o + (slot(i) * tile_rows + at_row) * D + d0)
+                    : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
+  float top = -INFINITY, sum = 0.0f;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  bool bad = false;
+  for (int s0 = 0; s0 < pieces; s0 += kWave) {
+    const int count = min(kWave, pieces - s0);
+    fetch(s0, s0 + count);
+    float m = -INFINITY, l = 0.0f;
+    if (lane < count) {
+      const float2 x = P.part_ml[slot(s0 + lane) * tile_rows + at_row];
+      m = x.x;
+      l = x.y;
+      if (P.status) bad |= P.part_bad[slot(s0 + lane)] != 0;
+    }
+    const float high = fmaxf(top, wave_max_dpp(m)), base = high == -INFINITY ? 0.0f : high;
+    const float a = __builtin_amdgcn_exp2f((top - base) * P.sl), f = __builtin_amdgcn_exp2f((m - base) * P.sl);
+    top = high;
+    sum = fmaf(sum, a, wave_reduce(l * f, [](float p, float q) { return p + q; }));
+    acc *= a;
+    for (int s = 0; s < count; s += kSide * kAhead) {
+      if (s > 0) fetch(s0 + s, s0 + count);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = s + u * kSide + side;
+        const float w = __shfl(f, min(i, count - 1));     // every lane takes part
+        if (i < count) acc += v[u] * w;
+      }
     }
   }
-  if (d0 < D) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = none ? 0.0f : o[j] * inv;
-    const long long at = (static_cast<long long>(b) * P.N + token) * P.c.H * P.G + h * P.G + (row - token * P.G);
+  for (int d = kLanes; d < kWave; d <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], d);
+  const bool none = !__any(word != 0) || sum == 0.0f;
+  const float f = none ? 0.0f : 1.0f / sum;
+  const long long at = (static_cast<long long>(b) * P.N + token) * P.c.H * P.G + h * P.G + (row - token * P.G);
+  if (side == 0) {
+    const float o[4] = {none ? 0.0f : acc[0] * f, none ? 0.0f : acc[1] * f, none ? 0.0f : acc[2] * f,
+                        none ? 0.0f : acc[3] * f};
     put4<T>(P.out + at * D * sizeof(T), d0, D, o);
-    if (P.lse && lane == 0) P.lse[at] = none ? -INFINITY : top * P.scale + logf(sum);
   }
-  const bool any = __any(bad != 0);
-  if (P.status && h == 0 && row == 0 && lane == 0) P.status[b] = any ? SPEC_ST_BAD_STATE : 0;
+  if (P.lse && lane == 0) P.lse[at] = none ? -INFINITY : top * P.scale + logf(sum);
+  if (P.status && h == 0 && row == 0) {
+    const bool any = __any(bad);
+    if (lane == 0) P.status[b] = any ? SPEC_ST_BAD_STATE : 0;
+  }
 }
 
 template <typename T, int DP, int RW>
@@ -168,21 +265,21 @@ void launch_tree(const Params &P, const Plan &p, hipStream_t s) {
   if constexpr (sizeof(T) * DP <= 256) launch_rows<T, DP, 1>(P, grid, s);
 }
 
+template <typename T, int DP>
+int launch_both(const Params &P, const Plan &p, hipStream_t s) {
+  (void)hipGetLastError();
+  launch_tree<T, DP>(P, p, s);
+  const int st = launch_status();
+  if (st != SPEC_OK) return st;
+  const int waves = kThreads / kWave, rows = P.B * P.c.H * P.N * P.G;
+  hipLaunchKernelGGL((join_kernel<T, DP>), dim3((rows + waves - 1) / waves), dim3(kThreads), 0, s, P, 32 * p.rw);
+  return launch_status();
+}
+
 template <typename T>
 int launch_all(const Params &P, const Plan &p, hipStream_t s) {
-  (void)hipGetLastError();
-  if (P.c.D <= 64)
-    launch_tree<T, 64>(P, p, s);
-  else if (P.c.D <= 128)
-    launch_tree<T, 128>(P, p, s);
-  else
-    launch_tree<T, 256>(P, p, s);
-  const int st = launch_status();
-  if (st != SPEC_OK || p.splits == 1) return st;
-  const long long rows = static_cast<long long>(P.B) * P.c.H * P.N * P.G;
-  const unsigned grid = static_cast<unsigned>((rows + kThreads / kWave - 1) / (kThreads / kWave));
-  hipLaunchKernelGGL(tree_join_kernel<T>, dim3(grid), dim3(kThreads), 0, s, P, p.tile_rows);
-  return launch_status();
+  if (P.c.D <= 64) return launch_both<T, 64>(P, p, s);
+  return P.c.D <= 128 ? launch_both<T, 128>(P, p, s) : launch_both<T, 256>(P, p, s);
 }
 
 int tree_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int planes, int B, int H,
@@ -199,10 +296,11 @@ int tree_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, in
   const long long tokens = static_cast<long long>(B) * N;
   if (tokens * H * G >= INT32_MAX) return SPEC_EINVAL;
   const Plan p = plan_of(B, N, H, G, D, cache_capacity(P.c), dt);
-  if (p.slots >= INT32_MAX) return SPEC_EINVAL;
+  if (p.tiles >= INT32_MAX || p.slots >= INT32_MAX) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const int words = (N + 31) / 32;
-  const size_t need = part_bytes(p, D);
+  const Space sp = space_of(p, D);
+  const size_t need = sp.end;
   const void *ins[] = {q, kv, table, end_col, kv_len, mask};
   const size_t in_n[] = {((tokens - 1) * static_cast<size_t>(q_stride) + hd) * elt,
                          cache_bytes(dt, L, planes, H, cols, D), paged ? b4 * max_pages : 0, paged ? 0u : 4u, b4,
@@ -215,20 +313,17 @@ int tree_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, in
     for (int j = o + 1; j < 4; ++j)
       if (overlaps(outs[o], out_n[o], outs[j], out_n[j])) return SPEC_EINVAL;
   }
-  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return SPEC_EWORKSPACE;
+  if (!ws || ws_bytes < need || !aligned(ws, 256)) return SPEC_EWORKSPACE;
   P.N = N;
   P.words = words;
   P.mask = mask;
-  P.splits = p.splits;
+  P.target = p.target;
   P.row_tiles = p.row_tiles;
-  if (need) {
-    char *w = static_cast<char *>(ws);
-    P.part_o = reinterpret_cast<float *>(w);
-    w += round_up(static_cast<size_t>(p.slots) * p.tile_rows * D * 4, 256);
-    P.part_ml = reinterpret_cast<float *>(w);
-    w += round_up(static_cast<size_t>(p.slots) * p.tile_rows * 8, 256);
-    P.part_bad = reinterpret_cast<int32_t *>(w);
-  }
+  char *w = static_cast<char *>(ws);
+  P.part_o = reinterpret_cast<float *>(w + sp.o);
+  P.part_ml = reinterpret_cast<float2 *>(w + sp.ml);
+  P.part_bad = reinterpret_cast<int32_t *>(w + sp.bad);
+  P.pieces = reinterpret_cast<int32_t *>(w + sp.pieces);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return dt == SPEC_BF16 ? launch_all<__bf16>(P, p, s) : launch_all<float>(P, p, s);
 }
@@ -244,7 +339,7 @@ extern "C" size_t spec_tree_attention_workspace_bytes(int B, int N, int H, int G
   if (dt != SPEC_F32 && dt != SPEC_BF16) return 0;
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return 0;
   if (static_cast<long long>(B) * N * H * G >= INT32_MAX) return 0;
-  return part_bytes(plan_of(B, N, H, G, D, max_rows, dt), D);
+  return space_of(plan_of(B, N, H, G, D, max_rows, dt), D).end;
 }
 
 extern "C" int spec_tree_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B, int H,

@@ -30,7 +30,7 @@ struct TreeMaskParams {
 __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(TreeMaskParams P) {
   __shared__ int refs[SPEC_TREE_MAX_N];                   // links that point to a node
   __shared__ int up[2][SPEC_TREE_MAX_N];                  // parent + N, or the sibling before; then ancestors
-  __shared__ uint32_t path[2][SPEC_TREE_MAX_N][kWords];
+  __shared__ uint32_t path[2][kWords][SPEC_TREE_MAX_N];  // word-major: neighbouring lanes, neighbouring banks
   __shared__ int bad;
   const int b = blockIdx.x, i = threadIdx.x, N = P.N;
   const bool in = i < N;
@@ -63,37 +63,33 @@ __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(TreeMaskParams 
   // Siblings to parents: after round t an entry has skipped 2^t siblings.  A
   // node that no link reaches, and its later siblings, end with none (-1);
   // so do the root's siblings.
-  int cur = 0;
-  for (int d = 1; d < N; d <<= 1) {
-    int x = up[cur][i];
+  // Every link points forward, so N entries settle in log2 N rounds; a round
+  // that finds nothing left to do is the last.
+  int cur = 0, x = up[0][i];
+  while (__syncthreads_or(x >= 0 && x < N)) {
     if (x >= 0 && x < N) x = up[cur][x];
-    up[cur ^ 1][i] = x;
     cur ^= 1;
-    __syncthreads();
+    up[cur][i] = x;
   }
   // Paths, doubled along the parents.  anc: the ancestor 2^t above, or -1.
-  int anc = up[cur][i];
-  anc = anc >= N ? anc - N : -1;
-  __syncthreads();
+  int anc = x >= N ? x - N : -1;
   uint32_t w[kWords];
 #pragma unroll
   for (int k = 0; k < kWords; ++k) w[k] = (i >> 5) == k && in ? 1u << (i & 31) : 0u;
-  cur = 0;
-  for (int d = 1; d < N; d <<= 1) {
+  for (;;) {
+    cur ^= 1;
     up[cur][i] = anc;
 #pragma unroll
     for (int k = 0; k < kWords; ++k)
-      if (k < P.words) path[cur][i][k] = w[k];
-    __syncthreads();
+      if (k < P.words) path[cur][k][i] = w[k];
+    if (!__syncthreads_or(anc >= 0)) break;
     if (anc >= 0) {
 #pragma unroll
       for (int k = 0; k < kWords; ++k)
-        if (k < P.words) w[k] |= path[cur][anc][k];
+        if (k < P.words) w[k] |= path[cur][k][anc];
       anc = up[cur][anc];
     }
-    cur ^= 1;
   }
-  __syncthreads();
   // A path that does not start at the root belongs to no branch of the tree.
   const bool linked = in && (w[0] & 1u) && !bad;
   int depth = -1;

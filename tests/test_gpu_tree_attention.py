@@ -38,10 +38,54 @@ def _call(q, cache, kv, layer, n, mask, B, N, scale=None, lse=True, stream=None,
     st = torch.full((B,), -7, dtype=torch.int32, device=DEV)
     code = sv.SPEC_BF16 if cache.dt == "bf16" else sv.SPEC_F32
     need = sv.spec_tree_attention_workspace_bytes(B, N, H, G, D, cache.max_rows(), code)
-    ws = torch.full((max(need, 256),), 0xFF, dtype=torch.uint8, device=DEV) if ws is None else ws
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) if ws is None else ws
     f = sv.spec_tree_attention_paged if cache.page else sv.spec_tree_attention
     f(q, kv, layer, cache.where(), i32(n), out, ws, mask=mask, scale=scale, lse=l, status=st, stream=stream)
     return out, l, st
+
+
+def _near(a, b):
+    """Equal but for roundings (the batch's lengths cut the rows elsewhere).  Both are within the
+    rounding of P (half a bf16 step, 2^-8, of a mean of |v| < 4) and of the stored value (2^-8 of
+    less than 4, its half step) of the exact result."""
+    return float((a.float() - b.float()).abs().max()) <= 2 * (4 * 2.0 ** -8 + 4 * 2.0 ** -8)
+
+
+def _see(rng, kind, B, N):
+    """[B, N, N] visibility among the nodes; kind: chain (no mask), tree, any."""
+    if kind == "chain":
+        return np.tril(np.ones((N, N), bool))[None].repeat(B, 0)
+    if kind == "any":
+        return rng.random((B, N, N)) < 0.3               # some rows may be empty
+    see = np.zeros((B, N, N), bool)
+    for b in range(B):
+        _, fc, ns = W.random_tree(rng, N, 1 + b % 5)
+        see[b] = oracle.tree_paths(fc[None], ns[None], [0])[1][0]
+    return see
+
+
+def _whole(see, n):
+    """Visibility over the cached rows and the nodes; a row of no bits sees nothing."""
+    return [np.concatenate([np.repeat(s.any(1)[:, None], int(x), 1), s], 1) for s, x in zip(see, n)]
+
+
+def _call(q, cache, kv, layer, n, mask, B, N, scale=None, lse=True, stream=None, ws=None, out=None):
+    H, D, G = cache.H, cache.D, q.shape[-2] // cache.H
+    out = torch.full((B, N, H * G, D), 7.0, dtype=q.dtype, device=DEV) if out is None else out
+    l = torch.full((B, N, H * G), 7.0, device=DEV) if lse else None
+    st = torch.full((B,), -7, dtype=torch.int32, device=DEV)
+    code = sv.SPEC_BF16 if cache.dt == "bf16" else sv.SPEC_F32
+    need = sv.spec_tree_attention_workspace_bytes(B, N, H, G, D, cache.max_rows(), code)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) if ws is None else ws
+    f = sv.spec_tree_attention_paged if cache.page else sv.spec_tree_attention
+    f(q, kv, layer, cache.where(), i32(n), out, ws, mask=mask, scale=scale, lse=l, status=st, stream=stream)
+    return out, l, st
+
+
+def _near(a, b):
+    """Equal but for roundings (the batch's lengths cut the rows elsewhere): two bf16 steps of values
+    below 4."""
+    return float((a.float() - b.float()).abs().max()) <= 4 * 2.0 ** -7
 
 
 def _check(seed, dt, n, N, H, G, D, page, kind, L=2, sd=1.0, scale=None, spoil=None, strided=False):
@@ -157,7 +201,7 @@ def test_states_out_of_range():
     good, _, _ = _call(q, cache, kv, 0, [20] * 4, None, 4, N)
     out, l, st = _call(q, cache, kv, 0, [20, cache.E + 1, -1, 20], None, 4, N)
     assert st.cpu().tolist() == [0, sv.SPEC_ST_BAD_STATE, sv.SPEC_ST_BAD_STATE, 0]
-    assert torch.equal(out[[0, 3]], good[[0, 3]]) and float(out[1:3].float().abs().max()) == 0.0
+    assert _near(out[[0, 3]], good[[0, 3]]) and float(out[1:3].float().abs().max()) == 0.0
     assert bool((l[1:3] == -np.inf).all())
     cache.E = cache.kv.shape[4] - N + 1
     out, l, st = _call(q, cache, kv, 0, [20] * 4, None, 4, N)
@@ -169,7 +213,7 @@ def test_states_out_of_range():
         paged.table[1, 0] = paged.kv.shape[2]
         out, _, st = _call(q3, paged, kv3, 0, [n0, n0, paged.max_rows()], None, 3, N)
         assert st.cpu().tolist() == [0, sv.SPEC_ST_BAD_STATE, sv.SPEC_ST_CAPACITY]
-        assert torch.equal(out[0], good[0]) and float(out[2].float().abs().max()) == 0.0
+        assert _near(out[0], good[0]) and float(out[2].float().abs().max()) == 0.0
 
 
 def test_offsets_past_32_bits():

@@ -26,6 +26,7 @@ namespace specv {
 namespace attn {
 
 constexpr int kThreads = 256;
+constexpr float kSlack = 8.0f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -135,7 +136,8 @@ struct Rows {
   typedef typename std::conditional<sizeof(T) == 2, bf16x8, f32x4>::type QV;
   QV q[kQ];
   f32x16 o[DP / 32];
-  float m, l;                 // maximum of q.k so far; this half's sum (the whole sum after walk())
+  float m, l;                 // reference maximum of q.k; this half's sum
+  float base;                 // m * scale * log2(e), 0 while m is -inf
 };
 
 // What a wave holds of its rows once the walk is over: with KW waves on the same
@@ -149,54 +151,86 @@ struct Done {
 };
 
 // Brings K and V tiles from the cache straight into LDS.  A wave's load writes
-// 64 consecutive 16-byte places, so the lane takes the chunk whose place its
-// own is.  Chunks past D are never loaded: they stay zero (clear()).
+// 64 consecutive 16-byte places, so a lane takes the chunk whose place its own
+// is.  Where a tile's rows all exist and the kRows rows of a load lie in one
+// page, the address is a scalar base and an offset that the lane keeps; else
+// (the last tile, odd page sizes) each lane finds its row.  Chunks past D are
+// never loaded: they stay zero (clear()).
 template <typename T, int DP, int RW, bool PAGED>
 struct Loader {
   using S = Shape<T, DP, RW>;
+  static constexpr int kRows = kWave / S::kChunks;        // rows of one wave's load
   const Params &P;
   const Job &J;
-  int page[S::kLoads];
-  int bad;
+  int wave, lrow, c0;                                     // the lane's row in a load, and its chunk in the first
+  int page;                                               // lane i: the page of load i of the next tile
+  bool steady, bad;
 
-  __device__ Loader(const Params &p, const Job &j) : P(p), J(j), bad(0) {}
-  static __device__ int row(int i) { return (i * kThreads + threadIdx.x) / S::kChunks; }
-  static __device__ int chunk(int i) { return threadIdx.x % S::kChunks ^ turn<S::kChunks>(row(i)); }
-  __device__ int at(int t, int i) const { return min(t * S::kKT + row(i), J.total - 1); }
+  __device__ Loader(const Params &p, const Job &j) : P(p), J(j), page(0), bad(false) {
+    const int lane = threadIdx.x & (kWave - 1);
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    lrow = lane / S::kChunks;
+    c0 = lane % S::kChunks ^ turn<S::kChunks>(wave * kRows + lrow);
+    steady = !PAGED || P.c.cols % kRows == 0;
+  }
+  // first row of load i of tile t, and the lane's chunk in it (turn() of rows 4 kRows apart: an xor)
+  __device__ int row(int t, int i) const { return t * S::kKT + (4 * i + wave) * kRows; }
+  __device__ int chunk(int i) const { return c0 ^ turn<S::kChunks>(4 * kRows * i); }
+  __device__ bool has(int i) const { return DP == P.c.D || chunk(i) * S::kVec < P.c.D; }
   __device__ void clear(char *buf) const {
     if (P.c.D == DP) return;
     for (int x = threadIdx.x; x < S::kLds / 16; x += kThreads) reinterpret_cast<u32x4 *>(buf)[x] = u32x4{0, 0, 0, 0};
   }
+  __device__ int page_of(int r) const {
+    return P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, r)];
+  }
+  __device__ int checked(int plane) {
+    const bool ok = plane >= 0 && plane < P.c.planes;
+    bad |= !ok;
+    return ok ? plane : 0;
+  }
   __device__ void pages(int t) {
-    if constexpr (PAGED) {
+    if constexpr (PAGED) page = page_of(min(row(t, threadIdx.x & (S::kLoads - 1)), J.total - 1));
+  }
+  __device__ void bring(const char *k, const char *v, int i, char *buf) const {
+    typedef __attribute__((address_space(3))) char *Lds;
+    typedef const __attribute__((address_space(1))) char *Global;
+    char *to = buf + (i * kThreads + wave * kWave) * 16;
+    __builtin_amdgcn_global_load_lds((Global)k, (Lds)to, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((Global)v, (Lds)(to + S::kTile), 16, 0, 0);
+  }
+  template <bool FULL>                                    // FULL: D == DP, every chunk exists
+  __device__ void load_steady(int t, char *buf) {
+    const int row_bytes = P.c.D * S::kElt;
 #pragma unroll
-      for (int i = 0; i < S::kLoads; ++i)
-        page[i] = P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, at(t, i))];
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int r = row(t, i);
+      int plane = J.b, col = J.start_col + r;
+      if constexpr (PAGED) {
+        plane = checked(read_lane(page, i));
+        col = r - cache_page(P.c, r) * P.c.cols;
+      }
+      const long long off = cache_offset(P.c, plane, J.h, col, S::kElt);
+      const uint32_t mine = lrow * row_bytes + chunk(i) * 16;
+      if (FULL || has(i)) bring(P.c.k + off + mine, P.c.v + off + mine, i, buf);
     }
   }
   __device__ void load(int t, char *buf) {
-    typedef __attribute__((address_space(3))) char *Lds;
-    typedef const __attribute__((address_space(1))) char *Global;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if ((t + 1) * S::kKT <= J.total && steady) {
+      if (P.c.D == DP) load_steady<true>(t, buf);
+      else load_steady<false>(t, buf);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      const int r = at(t, i);
+      const int r = min(row(t, i) + lrow, J.total - 1);
       int plane = J.b, col = J.start_col + r;
       if constexpr (PAGED) {
-        plane = page[i];
+        plane = checked(page_of(r));
         col = r - cache_page(P.c, r) * P.c.cols;
-        if (plane < 0 || plane >= P.c.planes) {
-          bad = 1;
-          plane = 0;
-        }
       }
-      const int c = chunk(i);
-      if (DP == P.c.D || c * S::kVec < P.c.D) {
-        const long long off = cache_offset(P.c, plane, J.h, col, S::kElt) + c * 16;
-        char *to = buf + (i * kThreads + wave * kWave) * 16;
-        __builtin_amdgcn_global_load_lds((Global)(P.c.k + off), (Lds)to, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((Global)(P.c.v + off), (Lds)(to + S::kTile), 16, 0, 0);
-      }
+      const long long off = cache_offset(P.c, plane, J.h, col, S::kElt) + chunk(i) * 16;
+      if (has(i)) bring(P.c.k + off, P.c.v + off, i, buf);
     }
   }
   // Takes infinities and NaNs out of the lane's own chunks of a V tile.
@@ -261,25 +295,57 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
   const int lane = threadIdx.x & (kWave - 1), n = lane & 31, hf = lane >> 5;
   const char *ldk = lds, *ldv = lds + S::kTile;
   f32x16 s[S::kNB];
-  const int ka = fresh((kb0 + n) * kRow + ((hf ^ turn<S::kChunks>(n)) << 4));
 #pragma unroll
-  for (int nb = 0; nb < S::kNB; ++nb) {
+  for (int nb = 0; nb < S::kNB; ++nb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[nb][r] = 0.0f;
-    if constexpr (S::kElt == 2) {
+  const int ka = fresh((kb0 + n) * kRow + ((hf ^ turn<S::kChunks>(n)) << 4));
+  const int i16 = lane & 15, dg = (lane >> 4) & 1, r0 = 4 * hf + (i16 >> 2);
+  const int va16 = fresh((kb0 + r0) * kRow + (((2 * dg + ((i16 & 3) >> 1)) ^ turn<S::kChunks>(r0)) << 4) + (i16 & 1) * 8);
+  bf16x8 v[2][DP / 32];                                   // V's operand for 16 rows, and the next 16
+  auto read_v = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db) {
+      const bf16x4b lo = read_turned(ldv + (va16 ^ (db << 6)) + 16 * t * kRow);
+      const bf16x4b hi = read_turned(ldv + (va16 ^ (db << 6 | 2 << 4)) + (16 * t + 8) * kRow);
+      v[t & 1][db] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+  };
+  if constexpr (S::kElt == 2) {
+    // All of a block's K operands are asked for before the first product, the
+    // next block's (or V's first) while the products run: left to itself the
+    // compiler asks for each just before its use and waits out the LDS latency
+    // sixteen times a tile.
+    auto read_k = [&](int nb, int d) __attribute__((always_inline)) {
+      return *reinterpret_cast<const bf16x8 *>(ldk + (ka ^ (d << 5)) + nb * 32 * kRow);
+    };
+    bf16x8 a[DP / 16];
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) a[d] = read_k(0, d);
+    __builtin_amdgcn_sched_group_barrier(0x100, DP / 16, 0);
+#pragma unroll
+    for (int nb = 0; nb < S::kNB; ++nb) {
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(ldk + (ka ^ (d << 5)) + nb * 32 * kRow);
-        s[nb] = mfma(a, W.q[d], s[nb]);
+        s[nb] = mfma(a[d], W.q[d], s[nb]);
+        if (nb + 1 < S::kNB) a[d] = read_k(nb + 1, d);
       }
-    } else {
+      if (nb + 1 == S::kNB) read_v(0);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int nb = 0; nb < S::kNB; ++nb)
 #pragma unroll
       for (int d = 0; d < DP / 8; ++d) {
         const f32x4 a = *reinterpret_cast<const f32x4 *>(ldk + (ka ^ (d << 5)) + nb * 32 * kRow);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[nb] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], W.q[d][j], s[nb], 0, 0, 0);
       }
-    }
   }
   if constexpr (MASKED) {
 #pragma unroll
@@ -294,10 +360,24 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
   for (int nb = 0; nb < S::kNB; ++nb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[nb][r]);
-  const float m = fmaxf(W.m, half_max(mx));
-  const float base = m == -INFINITY ? 0.0f : m * sl;      // nothing seen yet: every exponent is -inf
-  const float alpha = __builtin_amdgcn_exp2f(fmaf(W.m, sl, -base));
-  W.m = m;
+  // The weights are exp(s - m) for a reference m that follows the maximum only
+  // when some row's has outgrown it by 2^kSlack: sums and weights stay within
+  // 2^kSlack of what the maximum itself would give, at the same relative
+  // precision, and most tiles leave the outputs as they are.
+  mx = half_max(mx);
+  if (__any(fmaf(mx, sl, -W.base) > kSlack || (W.m == -INFINITY && mx > -INFINITY))) {
+    const float m = fmaxf(W.m, mx);
+    const float base = m == -INFINITY ? 0.0f : m * sl;    // nothing seen yet: every exponent is -inf
+    const float alpha = __builtin_amdgcn_exp2f(fmaf(W.m, sl, -base));
+    W.m = m;
+    W.base = base;
+    W.l *= alpha;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) W.o[db][r] *= alpha;
+  }
+  const float base = W.base;
   float sum = 0.0f;
 #pragma unroll
   for (int nb = 0; nb < S::kNB; ++nb)
@@ -306,28 +386,18 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
       s[nb][r] = __builtin_amdgcn_exp2f(fmaf(s[nb][r], sl, -base));
       sum += s[nb][r];
     }
-  W.l = fmaf(W.l, alpha, sum);
-#pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) W.o[db][r] *= alpha;
+  W.l += sum;
 
   // O^T += V^T P^T
   if constexpr (S::kElt == 2) {
-    const int i = lane & 15, dg = (lane >> 4) & 1, r0 = 4 * hf + (i >> 2);
-    const int va = fresh((kb0 + r0) * kRow + (((2 * dg + ((i & 3) >> 1)) ^ turn<S::kChunks>(r0)) << 4) + (i & 1) * 8);
 #pragma unroll
     for (int t = 0; t < 2 * S::kNB; ++t) {
+      if (t + 1 < 2 * S::kNB) read_v(t + 1);
       bf16x8 p;
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = static_cast<__bf16>(s[t / 2][8 * (t % 2) + j]);
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) {
-        const bf16x4b lo = read_turned(ldv + (va ^ (db << 6)) + 16 * t * kRow);
-        const bf16x4b hi = read_turned(ldv + (va ^ (db << 6 | 2 << 4)) + (16 * t + 8) * kRow);
-        const bf16x8 a = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        W.o[db] = mfma(a, p, W.o[db]);
-      }
+      for (int db = 0; db < DP / 32; ++db) W.o[db] = mfma(v[t & 1][db], p, W.o[db]);
     }
   } else {
     const int va = fresh((kb0 + 4 * hf) * kRow + ((n / 4 ^ hf) << 4) + n % 4 * 4);
@@ -421,7 +491,7 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
 #pragma unroll
     for (int r = 0; r < 16; ++r) W.o[db][r] = 0.0f;
   W.m = -INFINITY;
-  W.l = 0.0f;
+  W.l = W.base = 0.0f;
   // cache rows below `plain` are seen by every row of the workgroup
   const int plain = !PROMPT && P.mask ? J.limit0 - 1 : J.limit0 + J.row0 / P.G;
   Loader<T, DP, RW, PAGED> ld(P, J);

@@ -5,7 +5,7 @@
 // on the path from the root to i, and stands at position n_b + depth(i).  Both
 // follow from parent(i): the path of i is {i} and the path of parent(i).
 //
-// Design.  One 256-lane workgroup per tree, one lane per node, everything in
+// Design.  One workgroup per tree, one lane per node, everything in
 // LDS.  Parents: the first child of i knows i; a later sibling finds its
 // parent through the run of siblings before it, by pointer jumping.  Paths:
 // sets of 256 bits, doubled along the parents (path of i |= path of the
@@ -18,6 +18,9 @@ namespace {
 
 constexpr int kTreeThreads = 256;
 constexpr int kWords = SPEC_TREE_MAX_N / 32;
+constexpr int kRounds = 12;   // log2(SPEC_TREE_MAX_N) and the last, empty one, and some
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct TreeMaskParams {
   int N, words;
@@ -30,13 +33,15 @@ struct TreeMaskParams {
 __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(TreeMaskParams P) {
   __shared__ int refs[SPEC_TREE_MAX_N];                   // links that point to a node
   __shared__ int up[2][SPEC_TREE_MAX_N];                  // parent + N, or the sibling before; then ancestors
-  __shared__ uint32_t path[2][kWords][SPEC_TREE_MAX_N];  // word-major: neighbouring lanes, neighbouring banks
+  __shared__ u32x4 path[2][SPEC_TREE_MAX_N][kWords / 4];
+  __shared__ int more[2][kRounds];                        // whether a round has work, by phase
   __shared__ int bad;
   const int b = blockIdx.x, i = threadIdx.x, N = P.N;
   const bool in = i < N;
   refs[i] = 0;
   up[0][i] = -1;
   if (i == 0) bad = 0;
+  if (i < 2 * kRounds) more[i / kRounds][i % kRounds] = 0;
   const int fc = in ? P.first_child[static_cast<long long>(b) * N + i] : -1;
   const int ns = in ? P.next_sibling[static_cast<long long>(b) * N + i] : -1;
   const int n = P.kv_len[b];
@@ -66,41 +71,44 @@ __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(TreeMaskParams 
   // Every link points forward, so N entries settle in log2 N rounds; a round
   // that finds nothing left to do is the last.
   int cur = 0, x = up[0][i];
-  while (__syncthreads_or(x >= 0 && x < N)) {
+  for (int r = 0; r < kRounds; ++r) {
+    if (x >= 0 && x < N) more[0][r] = 1;
+    __syncthreads();
+    if (!more[0][r]) break;
     if (x >= 0 && x < N) x = up[cur][x];
     cur ^= 1;
     up[cur][i] = x;
   }
   // Paths, doubled along the parents.  anc: the ancestor 2^t above, or -1.
   int anc = x >= N ? x - N : -1;
-  uint32_t w[kWords];
+  u32x4 w[kWords / 4];
 #pragma unroll
-  for (int k = 0; k < kWords; ++k) w[k] = (i >> 5) == k && in ? 1u << (i & 31) : 0u;
-  for (;;) {
+  for (int k = 0; k < kWords; ++k) w[k / 4][k % 4] = (i >> 5) == k && in ? 1u << (i & 31) : 0u;
+  for (int r = 0; r < kRounds; ++r) {
     cur ^= 1;
     up[cur][i] = anc;
-#pragma unroll
-    for (int k = 0; k < kWords; ++k)
-      if (k < P.words) path[cur][k][i] = w[k];
-    if (!__syncthreads_or(anc >= 0)) break;
+    path[cur][i][0] = w[0];
+    if (P.words > 4) path[cur][i][1] = w[1];
+    if (anc >= 0) more[1][r] = 1;
+    __syncthreads();
+    if (!more[1][r]) break;
     if (anc >= 0) {
-#pragma unroll
-      for (int k = 0; k < kWords; ++k)
-        if (k < P.words) w[k] |= path[cur][k][anc];
+      w[0] |= path[cur][anc][0];
+      if (P.words > 4) w[1] |= path[cur][anc][1];
       anc = up[cur][anc];
     }
   }
   // A path that does not start at the root belongs to no branch of the tree.
-  const bool linked = in && (w[0] & 1u) && !bad;
+  const bool linked = in && (w[0][0] & 1u) && !bad;
   int depth = -1;
 #pragma unroll
-  for (int k = 0; k < kWords; ++k) depth += __popc(w[k]);
+  for (int k = 0; k < kWords; ++k) depth += __popc(w[k / 4][k % 4]);
   if (in) {
     const long long node = static_cast<long long>(b) * N + i;
     P.positions[node] = n + (linked ? depth : 0);
 #pragma unroll
     for (int k = 0; k < kWords; ++k)
-      if (k < P.words) P.mask[node * P.words + k] = linked ? w[k] : 0u;
+      if (k < P.words) P.mask[node * P.words + k] = linked ? w[k / 4][k % 4] : 0u;
   }
   if (i == 0 && P.status) P.status[b] = bad || n < 0 ? SPEC_ST_BAD_STATE : 0;
 }
@@ -131,6 +139,6 @@ extern "C" int spec_tree_mask(int B, int N, const int32_t *first_child, const in
   }
   TreeMaskParams P{N, words, first_child, next_sibling, kv_len, positions, mask, status};
   (void)hipGetLastError();
-  hipLaunchKernelGGL(tree_mask_kernel, dim3(B), dim3(kTreeThreads), 0, static_cast<hipStream_t>(stream), P);
+  hipLaunchKernelGGL(tree_mask_kernel, dim3(B), dim3(static_cast<unsigned>(round_up(N, kWave))), 0, static_cast<hipStream_t>(stream), P);
   return launch_status();
 }

@@ -366,9 +366,16 @@ def _place(t, stream):
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensor must be on the GPU")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev, (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if dev != _current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+# The current device, and a device's current stream as a plain handle: what torch.cuda.current_device()
+# and torch.cuda.current_stream(d).cuda_stream give, without building a Stream object (1.1 us a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _need(t, dtype, numel: int, name: str, dev: int, optional: bool = False):
@@ -377,15 +384,15 @@ def _need(t, dtype, numel: int, name: str, dev: int, optional: bool = False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.numel() >= numel and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} needs at least {numel} elements, has {t.numel()}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, not {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def spec_tree_mask(first_child, next_sibling, kv_len, positions, mask, *, status=None, stream=None) -> None:
@@ -463,10 +470,13 @@ def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens
         sizes = (planes, H, cols, D, int(layer), T, B, N, G, _need(where, i32, B, "block_table", dev), where.shape[1])
     else:
         sizes = (planes, H, cols, D, int(layer), T, N, G, _need(where, i32, 1, "end_col", dev))
+    dt = kv.dtype
     code = getattr(library(), name)(
         qp, qs, kp, ks, vp, vs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
-        _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev, True), _need(positions, i32, T, "positions", dev, True),
-        _need(q_weight, kv.dtype, D, "q_weight", dev, True), _need(k_weight, kv.dtype, D, "k_weight", dev, True),
+        None if cu_seqlens is None else _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev),
+        None if positions is None else _need(positions, i32, T, "positions", dev),
+        None if q_weight is None else _need(q_weight, dt, D, "q_weight", dev),
+        None if k_weight is None else _need(k_weight, dt, D, "k_weight", dev),
         eps, _need(inv_freq, torch.float32, 0, "inv_freq", dev) if rot else None, rot, 1 if interleaved else 0,
         _same_size(q_out, kv, T * H * G * D, "q_out", dev), _need(status, i32, B, "status", dev, True), s)
     _check(code, name)

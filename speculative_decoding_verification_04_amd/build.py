@@ -9,6 +9,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,25 +25,37 @@ def hipcc() -> str:
     return exe
 
 
-def command(out: str = LIB) -> list:
-    srcs = sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
-    return [hipcc(), "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
+def sources() -> list:
+    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
+
+
+def command(src: str, out: str) -> list:
+    """Compile one source to an object."""
+    return [hipcc(), "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-c",
             # packed fp32 instructions stay off on this target
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-command-line-argument",
             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
-            *srcs, "-o", out]
+            src, "-o", out]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
+def _run(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"hipcc failed with exit code {r.returncode}")
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (up to eight at a time) and link the library."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as work:
+        pairs = [(s, os.path.join(work, os.path.basename(s) + ".o")) for s in sources()]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda p: _run(command(*p), verbose), pairs))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *(o for _, o in pairs), "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -156,7 +156,8 @@ struct Done {
 // page, the address is a scalar base and an offset that the lane keeps; else
 // (the last tile, odd page sizes) each lane finds its row.  Chunks past D are
 // never loaded: they stay zero (clear()).
-template <typename T, int DP, int RW, bool PAGED>
+// ONCE: the rows are read by one workgroup and not soon again: non-temporal.
+template <typename T, int DP, int RW, bool PAGED, bool ONCE>
 struct Loader {
   using S = Shape<T, DP, RW>;
   static constexpr int kRows = kWave / S::kChunks;        // rows of one wave's load
@@ -196,8 +197,8 @@ struct Loader {
     typedef __attribute__((address_space(3))) char *Lds;
     typedef const __attribute__((address_space(1))) char *Global;
     char *to = buf + (i * kThreads + wave * kWave) * 16;
-    __builtin_amdgcn_global_load_lds((Global)k, (Lds)to, 16, 0, 0);
-    __builtin_amdgcn_global_load_lds((Global)v, (Lds)(to + S::kTile), 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((Global)k, (Lds)to, 16, 0, ONCE ? 2 : 0);
+    __builtin_amdgcn_global_load_lds((Global)v, (Lds)(to + S::kTile), 16, 0, ONCE ? 2 : 0);
   }
   template <bool FULL>                                    // FULL: D == DP, every chunk exists
   __device__ void load_steady(int t, char *buf) {
@@ -463,7 +464,7 @@ __device__ inline void put4(char *out, int d0, int D, const float (&x)[4]) {
 
 // The walk of one job.  The waves kw == 0 return with their rows' unscaled
 // outputs, maxima and sums; all return whether a bad page was met.
-template <typename T, int DP, int RW, bool PAGED, bool PROMPT>
+template <typename T, int DP, int RW, bool PAGED, bool PROMPT, bool ONCE>
 __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP, RW>::kKW> &D, char *buf0,
                             char *buf1) {
   using S = Shape<T, DP, RW>;
@@ -494,7 +495,7 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
   W.l = W.base = 0.0f;
   // cache rows below `plain` are seen by every row of the workgroup
   const int plain = !PROMPT && P.mask ? J.limit0 - 1 : J.limit0 + J.row0 / P.G;
-  Loader<T, DP, RW, PAGED> ld(P, J);
+  Loader<T, DP, RW, PAGED, ONCE> ld(P, J);
   ld.clear(buf0);
   ld.clear(buf1);
   if (P.c.D != DP) __syncthreads();

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
   J.t0 = 0;
   J.t1 = (J.limit0 + last + S::kKT - 1) / S::kKT;
   Done<DP, 1> W;
-  const bool bad = walk<T, DP, kRW, PAGED, true>(P, J, W, buf0, buf1);
+  const bool bad = walk<T, DP, kRW, PAGED, true, false>(P, J, W, buf0, buf1);
   put_rows<T>(P, J, W, true);
   if (reports && threadIdx.x == 0) P.status[w.b] = bad ? SPEC_ST_BAD_STATE : 0;
 }

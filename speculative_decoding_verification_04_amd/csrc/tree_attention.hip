@@ -84,7 +84,7 @@ __device__ inline int tree_tiles(const Params &P, int n, int E, int kt) {
   return tree_status(P, n, E) ? 0 : static_cast<int>((static_cast<long long>(n) + P.N + kt - 1) / kt);
 }
 
-template <typename T, int DP, int RW, bool PAGED>
+template <typename T, int DP, int RW, bool PAGED, bool ONCE>
 __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2 : 1) void tree_kernel(Params P) {
   using S = Shape<T, DP, RW>;
   __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
     J.t0 = static_cast<int>(static_cast<long long>(tiles) * i / pieces);
     J.t1 = static_cast<int>(static_cast<long long>(tiles) * (i + 1) / pieces);
     Done<DP, S::kKW> D;
-    const bool bad = walk<T, DP, RW, PAGED, false>(P, J, D, buf0, buf1);
+    const bool bad = walk<T, DP, RW, PAGED, false, ONCE>(P, J, D, buf0, buf1);
     if (pieces == 1) {
       put_rows<T>(P, J, D, sees_any(P, J.b, D.token));
       if (P.status && J.h == 0 && J.row0 == 0 && threadIdx.x == 0) P.status[J.b] = bad ? SPEC_ST_BAD_STATE : 0;
@@ -190,11 +190,12 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Params P, int tile_rows)
   const int token = row / P.G;
   uint32_t word = 1;
   if (P.mask) word = lane < P.words ? P.mask[(static_cast<long long>(b) * P.N + token) * P.words + lane] : 0u;
-  // eight pieces' rows or so (DP = 128), asked for before their weights are known
+  // up to eight pieces' rows (DP = 128), asked for before their weights are known
   f32x4 v[kAhead];
   auto fetch = [&](int s, int end) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      if (s + u * kSide >= end) break;
       const int i = min(s + u * kSide + side, end - 1);
       v[u] = d0 < D ? *reinterpret_cast<const f32x4 *>(P.part_o + (slot(i) * tile_rows + at_row) * D + d0)
                     : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -222,6 +223,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Params P, int tile_rows)
       if (s > 0) fetch(s0 + s, s0 + count);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
+        if (s + u * kSide >= count) break;
         const int i = s + u * kSide + side;
         const float w = __shfl(f, min(i, count - 1));     // every lane takes part
         if (i < count) acc += v[u] * w;
@@ -247,12 +249,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Params P, int tile_rows)
   }
 }
 
+template <typename T, int DP, int RW, bool ONCE>
+void launch_once(const Params &P, unsigned grid, hipStream_t s) {
+  if (P.c.table)
+    hipLaunchKernelGGL((tree_kernel<T, DP, RW, true, ONCE>), dim3(grid), dim3(kThreads), 0, s, P);
+  else
+    hipLaunchKernelGGL((tree_kernel<T, DP, RW, false, ONCE>), dim3(grid), dim3(kThreads), 0, s, P);
+}
+
+// Rows that one workgroup reads, of a layer too large to be found in the
+// Infinity Cache (256 MB) again, are read non-temporally: 75 us instead of 83
+// for 16-node trees over 32 sequences of 512 .. 4096 rows (300 MB) that rotate
+// over four caches.  Smaller layers lose by it (18 MB: 20.0 -> 21.3 us), and so do
+// rows that several row tiles share (294 -> 320 us).
 template <typename T, int DP, int RW>
 void launch_rows(const Params &P, unsigned grid, hipStream_t s) {
-  if (P.c.table)
-    hipLaunchKernelGGL((tree_kernel<T, DP, RW, true>), dim3(grid), dim3(kThreads), 0, s, P);
-  else
-    hipLaunchKernelGGL((tree_kernel<T, DP, RW, false>), dim3(grid), dim3(kThreads), 0, s, P);
+  if constexpr (sizeof(T) == 2) {
+    const long long planes = P.c.table ? P.c.planes : P.B;
+    if (P.row_tiles == 1 && planes * P.c.H * P.c.cols * P.c.D * 4 > (256ll << 20))
+      return launch_once<T, DP, RW, true>(P, grid, s);
+  }
+  launch_once<T, DP, RW, false>(P, grid, s);
 }
 
 template <typename T, int DP>

@@ -234,30 +234,30 @@ struct Loader {
       if (has(i)) bring(P.c.k + off, P.c.v + off, i, buf);
     }
   }
-  // Takes infinities and NaNs out of the lane's own chunks of a V tile.
+  // Takes infinities and NaNs out of the lane's own chunks of a V tile; whether
+  // there were any.  An exponent of all ones carries into the bit above it.
   __device__ bool clean(char *buf) const {
-    bool found = false;
+    u32x4 *own = reinterpret_cast<u32x4 *>(buf + S::kTile) + threadIdx.x;
+    constexpr uint32_t kExp = S::kElt == 2 ? 0x7f807f80u : 0x7f800000u, kOne = S::kElt == 2 ? 0x00800080u : 0x00800000u;
+    constexpr uint32_t kTop = S::kElt == 2 ? 0x80008000u : 0x80000000u;
+    uint32_t seen = 0;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      u32x4 *at = reinterpret_cast<u32x4 *>(buf + S::kTile) + i * kThreads + threadIdx.x;
-      u32x4 x = *at;
-      bool any = false;
+      const u32x4 x = own[i * kThreads];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) seen |= (x[j] & kExp) + kOne;
+    }
+    if (!(seen & kTop)) return false;
+    for (int i = 0; i < S::kLoads; ++i) {
+      u32x4 x = own[i * kThreads];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (S::kElt == 2) {
-          const bool lo = (x[j] & 0x7f80u) == 0x7f80u, hi = (x[j] & 0x7f800000u) == 0x7f800000u;
-          any |= lo | hi;
-          x[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
-        } else {
-          const bool odd = (x[j] & 0x7f800000u) == 0x7f800000u;
-          any |= odd;
-          if (odd) x[j] = 0;
-        }
+        const uint32_t odd = ((x[j] & kExp) + kOne) & kTop;   // the top bit of each value to clear
+        x[j] &= S::kElt == 2 ? ~((odd >> 15) * 0xffffu) : odd ? 0u : ~0u;
       }
-      if (any) *at = x;
-      found |= any;
+      own[i * kThreads] = x;
     }
-    return found;
+    return true;
   }
 };
 
@@ -470,6 +470,15 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
   using S = Shape<T, DP, RW>;
   const int lane = fresh(threadIdx.x & (kWave - 1)), n = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rw = wave % RW, kw = wave / RW;
+  Loader<T, DP, RW, PAGED, ONCE> ld(P, J);
+  ld.clear(buf0);
+  ld.clear(buf1);
+  if (P.c.D != DP) __syncthreads();                       // the zeros are there
+  if (J.t0 < J.t1) {
+    ld.pages(J.t0);
+    ld.load(J.t0, buf0);
+    ld.pages(min(J.t0 + 1, J.t1 - 1));
+  }
   const int R = J.tokens * P.G;
   const int row = min(J.row0 + rw * 32 + n, R - 1);       // rows past the end repeat the last
   const int token = row / P.G, head = J.h * P.G + (row - token * P.G);
@@ -495,17 +504,11 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
   W.l = W.base = 0.0f;
   // cache rows below `plain` are seen by every row of the workgroup
   const int plain = !PROMPT && P.mask ? J.limit0 - 1 : J.limit0 + J.row0 / P.G;
-  Loader<T, DP, RW, PAGED, ONCE> ld(P, J);
-  ld.clear(buf0);
-  ld.clear(buf1);
-  if (P.c.D != DP) __syncthreads();
-  if (J.t0 < J.t1) {
-    ld.pages(J.t0);
-    ld.load(J.t0, buf0);
-    ld.pages(min(J.t0 + 1, J.t1 - 1));
-  }
   // Tile t is used from one buffer while tile t + 1 arrives in the other.
   const int kb0 = kw * 32 * S::kNB;
+  const int mid = min(J.t1, plain / S::kKT);              // tiles before it every row sees whole
+  __shared__ int flags[2];                                // V rows with infinities or NaNs; bad pages: once met, kept
+  if (threadIdx.x < 2) flags[threadIdx.x] = 0;
   auto begin = [&](int t, char *next) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): this wave's part of tile t is in LDS
     __syncthreads();                                      // everyone's is, and tile t - 1 is read
@@ -514,34 +517,54 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
       ld.pages(min(t + 2, J.t1 - 1));
     }
   };
-  auto tile = [&](int t, char *now, char *next) __attribute__((always_inline)) {
-    begin(t, next);
-    const uint32_t all[S::kNB] = {};
-    step<T, DP, RW, false>(W, now, kb0, P.sl, all);
-  };
-  int t = J.t0;
-  const int mid = min(J.t1, plain / S::kKT);              // tiles that every row sees whole
-  char *now = buf0, *next = buf1;
-  for (; t + 1 < mid; t += 2) {
-    tile(t, buf0, buf1);
-    tile(t + 1, buf1, buf0);
-  }
-  if (t < mid) {
-    tile(t++, buf0, buf1);
-    now = buf1;
-    next = buf0;
-  }
-  for (; t < J.t1; ++t) {
+  auto masked = [&](int t, char *now, char *next) __attribute__((always_inline)) {
     begin(t, next);
     uint32_t vis[S::kNB];
 #pragma unroll
-    for (int nb = 0; nb < S::kNB; ++nb) vis[nb] = seen<PROMPT>(P, J, token, t * S::kKT + kb0 + 32 * nb);
-    const bool odd = __syncthreads_or(ld.clean(now));
+    for (int nb = 0; nb < S::kNB; ++nb) vis[nb] = ~0u;
+    bool odd = false;
+    if (t >= mid) {
+#pragma unroll
+      for (int nb = 0; nb < S::kNB; ++nb) vis[nb] = seen<PROMPT>(P, J, token, t * S::kKT + kb0 + 32 * nb);
+      if (ld.clean(now)) flags[0] = 1;
+      __syncthreads();
+      odd = flags[0] != 0;
+    }
     step<T, DP, RW, true>(W, now, kb0, P.sl, vis);
     if (odd) add_odd<T, DP, RW, PAGED>(P, J, W, t * S::kKT + kb0, vis);
-    char *x = now;
-    now = next;
-    next = x;
+  };
+  int t = J.t0;
+  if constexpr (RW == 4) {
+    // bound by the matrix and vector units: whole tiles without the masks
+    auto whole = [&](int t, char *now, char *next) __attribute__((always_inline)) {
+      begin(t, next);
+      const uint32_t all[S::kNB] = {};
+      step<T, DP, RW, false>(W, now, kb0, P.sl, all);
+    };
+    char *now = buf0, *next = buf1;
+    for (; t + 1 < mid; t += 2) {
+      whole(t, buf0, buf1);
+      whole(t + 1, buf1, buf0);
+    }
+    if (t < mid) {
+      whole(t++, buf0, buf1);
+      now = buf1;
+      next = buf0;
+    }
+    for (; t < J.t1; ++t) {
+      masked(t, now, next);
+      char *x = now;
+      now = next;
+      next = x;
+    }
+  } else {
+    // bound by memory, or short: one code for all tiles, since the first pass of
+    // a wave through code that is not in the instruction cache takes longer than
+    // the masks (single-token calls end with a partial tile)
+    for (; t < J.t1; t += 2) {
+      masked(t, buf0, buf1);
+      if (t + 1 < J.t1) masked(t + 1, buf1, buf0);
+    }
   }
   W.l = half_sum(W.l);
   if constexpr (S::kKW > 1) {
@@ -590,7 +613,10 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
       D.o[q] = f32x4{W.o[q / 4][4 * (q % 4)], W.o[q / 4][4 * (q % 4) + 1], W.o[q / 4][4 * (q % 4) + 2],
                         W.o[q / 4][4 * (q % 4) + 3]};
   }
-  return PAGED && __syncthreads_or(ld.bad);
+  if (!PAGED || !P.status) return false;
+  if (ld.bad) flags[1] = 1;
+  __syncthreads();
+  return flags[1] != 0;
 }
 
 // Trees: whether a node's mask row has any bit (else it sees nothing at all).

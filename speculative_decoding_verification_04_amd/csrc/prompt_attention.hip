@@ -6,7 +6,7 @@
 // len sees rows [0, n_b - len + i].
 //
 // Design.  Bound by the matrix cores: 4 D flops a visible pair against the
-// 2 D bytes of a row, which a tile of 128 query rows uses 128 times.  The
+// 2 D bytes of a row, which a tile of 128 (or 64) query rows uses that often.  The
 // lengths are on the device, so the grid is the largest that T tokens in B
 // sequences can need, and a workgroup finds its (sequence, tile) by a scan over
 // the sequences' tile counts.  A sequence's tiles run from its last, the
@@ -16,9 +16,6 @@
 namespace specv {
 namespace {
 using namespace attn;
-
-constexpr int kRW = 4;
-constexpr int kTileRows = 32 * kRW;
 
 struct Where {
   int b, tile, tiles;
@@ -45,6 +42,7 @@ __device__ inline int prompt_status(const Params &P, int b, int len) {
 }
 
 // The sequence and tile of flat tile number f; b = -1 past the last.
+template <int kTileRows>
 __device__ inline Where find_tile(const Params &P, int f) {
   const int lane = threadIdx.x & (kWave - 1);
   int base = 0;
@@ -65,9 +63,10 @@ __device__ inline Where find_tile(const Params &P, int f) {
   return Where{-1, 0, 0};
 }
 
-template <typename T, int DP, bool PAGED>
-__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void prompt_kernel(Params P) {
-  using S = Shape<T, DP, kRW>;
+template <typename T, int DP, int RW, bool PAGED>
+__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2 : 1) void prompt_kernel(Params P) {
+  using S = Shape<T, DP, RW>;
+  constexpr int kTileRows = 32 * RW;
   __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
   __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
   const int H = P.c.H;
@@ -79,7 +78,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
       if (len <= 0) P.status[b] = prompt_status(P, b, len);
     }
   }
-  const Where w = find_tile(P, f);
+  const Where w = find_tile<kTileRows>(P, f);
   if (w.b < 0) return;
   Job J;
   const int len = prompt_len(P, w.b), st = prompt_status(P, w.b, len), n = P.c.kv_len[w.b];
@@ -100,19 +99,39 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 ? 2 : 1) void
   const int last = min((J.row0 + kTileRows - 1) / P.G, len - 1);      // the tile's last token
   J.t0 = 0;
   J.t1 = (J.limit0 + last + S::kKT - 1) / S::kKT;
-  Done<DP, 1> W;
-  const bool bad = walk<T, DP, kRW, PAGED, true, false>(P, J, W, buf0, buf1);
+  Done<DP, S::kKW> W;
+  const bool bad = walk<T, DP, RW, PAGED, true, false>(P, J, W, buf0, buf1);
   put_rows<T>(P, J, W, true);
   if (reports && threadIdx.x == 0) P.status[w.b] = bad ? SPEC_ST_BAD_STATE : 0;
 }
 
-template <typename T, int DP>
-int launch_prompt(const Params &P, unsigned grid, hipStream_t s) {
+// Workgroups that T tokens in B sequences can need with rw waves side by side:
+// each sequence rounds up once.
+inline long long prompt_grid(int T, int B, int H, int G, int rw) {
+  return (static_cast<long long>(T) * G / (32 * rw) + B) * H;
+}
+
+template <typename T, int DP, int RW>
+int launch_rows(const Params &P, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(prompt_grid(P.T, P.B, P.c.H, P.G, RW)));
   if (P.c.table)
-    hipLaunchKernelGGL((prompt_kernel<T, DP, true>), dim3(grid), dim3(kThreads), 0, s, P);
+    hipLaunchKernelGGL((prompt_kernel<T, DP, RW, true>), grid, dim3(kThreads), 0, s, P);
   else
-    hipLaunchKernelGGL((prompt_kernel<T, DP, false>), dim3(grid), dim3(kThreads), 0, s, P);
+    hipLaunchKernelGGL((prompt_kernel<T, DP, RW, false>), grid, dim3(kThreads), 0, s, P);
   return launch_status();
+}
+
+// Few rows take 64 to a workgroup, two waves behind each other: with fewer than
+// 384 tiles of 128 the chip has workgroups to spare, and a tile's walk is
+// shorter.  One prompt of 500 / 1000 / 2000 tokens (32 heads of 128, bf16): 14.2 /
+// 25.3 / 62.3 us against 16.1 / 26.1 / 51.4 with 128 rows; 4 prompts of up to 400
+// tokens (8 heads of 128, float32): 40 against 61.
+template <typename T, int DP>
+int launch_prompt(const Params &P, hipStream_t s) {
+  if constexpr (sizeof(T) * DP <= 512) {
+    if (static_cast<long long>(P.T) * P.G * P.c.H < 384 * 128) return launch_rows<T, DP, 2>(P, s);
+  }
+  return launch_rows<T, DP, 4>(P, s);
 }
 
 int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int planes, int B, int H,
@@ -125,8 +144,7 @@ int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, 
                        kv_len, scale, out, lse, status);
   if (err) return err;
   if (T < 1) return SPEC_EINVAL;
-  const long long tiles = (static_cast<long long>(T) * G) / kTileRows + B;   // each sequence rounds up once
-  if (static_cast<long long>(T) * G >= INT32_MAX || tiles * H >= INT32_MAX) return SPEC_EINVAL;
+  if (static_cast<long long>(T) * G >= INT32_MAX || prompt_grid(T, B, H, G, 2) >= INT32_MAX) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const void *ins[] = {q, kv, table, end_col, kv_len, cu};
   const size_t in_n[] = {((T - 1) * static_cast<size_t>(q_stride) + hd) * elt, cache_bytes(dt, L, planes, H, cols, D),
@@ -141,14 +159,13 @@ int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, 
   }
   P.T = T;
   P.cu = cu;
-  const unsigned grid = static_cast<unsigned>(tiles * H);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (dt == SPEC_BF16)
-    return D <= 64 ? launch_prompt<__bf16, 64>(P, grid, s)
-                   : D <= 128 ? launch_prompt<__bf16, 128>(P, grid, s) : launch_prompt<__bf16, 256>(P, grid, s);
-  return D <= 64 ? launch_prompt<float, 64>(P, grid, s)
-                 : D <= 128 ? launch_prompt<float, 128>(P, grid, s) : launch_prompt<float, 256>(P, grid, s);
+    return D <= 64 ? launch_prompt<__bf16, 64>(P, s)
+                   : D <= 128 ? launch_prompt<__bf16, 128>(P, s) : launch_prompt<__bf16, 256>(P, s);
+  return D <= 64 ? launch_prompt<float, 64>(P, s)
+                 : D <= 128 ? launch_prompt<float, 128>(P, s) : launch_prompt<float, 256>(P, s);
 }
 
 }  // namespace

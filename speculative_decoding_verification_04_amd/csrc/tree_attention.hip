@@ -135,8 +135,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
     J.limit0 = n + 1;
     J.total = n + P.N;
     J.start_col = PAGED ? 0 : E - n;
-    J.t0 = static_cast<int>(static_cast<long long>(tiles) * i / pieces);
-    J.t1 = static_cast<int>(static_cast<long long>(tiles) * (i + 1) / pieces);
+    const int size = tiles / pieces, more = tiles - size * pieces;   // the first `more` pieces are one tile longer
+    J.t0 = i * size + min(i, more);
+    J.t1 = J.t0 + size + (i < more ? 1 : 0);
     Done<DP, S::kKW> D;
     const bool bad = walk<T, DP, RW, PAGED, false, ONCE>(P, J, D, buf0, buf1);
     if (pieces == 1) {

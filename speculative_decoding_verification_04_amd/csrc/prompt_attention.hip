@@ -8,9 +8,8 @@
 // Design.  Bound by the matrix cores: 4 D flops a visible pair against the
 // 2 D bytes of a row, which a tile of 128 (or 64) query rows uses that often.  The
 // lengths are on the device, so the grid is the largest that T tokens in B
-// sequences can need, and a workgroup finds its (sequence, tile) by a scan over
-// the sequences' tile counts.  A sequence's tiles run from its last, the
-// longest walk, to its first.
+// sequences can need, and a workgroup finds its (sequence, tile) from the
+// sequences' tile counts.
 #include "attention.h"
 
 namespace specv {
@@ -42,14 +41,39 @@ __device__ inline int prompt_status(const Params &P, int b, int len) {
 }
 
 // The sequence and tile of flat tile number f; b = -1 past the last.
+// Where the workgroups do not all fit the chip at once, up to 64 sequences' tiles
+// are taken by their number, the highest (the longest walks) of all sequences
+// first, so that no long walk starts late: 8 prompts of 256 .. 2048 tokens (14
+// heads of 64) take 56 us and not 63.  Tiles numbered `level` and more are sum
+// max(0, tiles_b - level), and the level of tile f is found by halving.  Else
+// sequences follow each other, each from its last tile to its first.
 template <int kTileRows>
 __device__ inline Where find_tile(const Params &P, int f) {
   const int lane = threadIdx.x & (kWave - 1);
+  auto tiles_of = [&](int b) {
+    const int len = b < P.B ? prompt_len(P, b) : 0;
+    return len > 0 ? static_cast<int>((static_cast<long long>(len) * P.G + kTileRows - 1) / kTileRows) : 0;
+  };
+  if (P.B <= kWave && gridDim.x > 512) {
+    const int tiles = tiles_of(lane);
+    auto from = [&](int level) {
+      return wave_reduce(max(0, tiles - level), [](int x, int y) { return x + y; });
+    };
+    if (from(0) <= f) return Where{-1, 0, 0};
+    int lo = 0, hi = wave_max_i(tiles);                   // from(lo) > f >= from(hi) = 0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > f) lo = mid;
+      else hi = mid;
+    }
+    uint64_t who = __ballot(tiles > lo);
+    for (int skip = f - from(lo + 1); skip > 0; --skip) who &= who - 1;
+    const int b = __ffsll(static_cast<unsigned long long>(who)) - 1;
+    return Where{b, lo, read_lane(tiles, b)};
+  }
   int base = 0;
   for (int b0 = 0; b0 < P.B; b0 += kWave) {
-    const int b = b0 + lane;
-    const int len = b < P.B ? prompt_len(P, b) : 0;
-    const int tiles = len > 0 ? static_cast<int>((static_cast<long long>(len) * P.G + kTileRows - 1) / kTileRows) : 0;
+    const int tiles = tiles_of(b0 + lane);
     const int upto = wave_incl_scan(tiles);
     const uint64_t who = __ballot(base + upto > f);
     if (who) {

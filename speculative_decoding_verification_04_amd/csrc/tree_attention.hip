@@ -44,7 +44,8 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   p.row_tiles = static_cast<int>((R + 32 * p.rw - 1) / (32 * p.rw));
   p.groups = static_cast<long long>(B) * H * p.row_tiles;
   p.tiles = p.groups * ((max_rows + p.kt - 1) / p.kt);
-  p.target = 256 * (p.rw == 1 ? 1 : 2);                    // what the chip's LDS holds at once
+  // what the chip holds at once: two workgroups a CU where LDS and registers allow
+  p.target = p.rw > 1 && row <= 256 ? 512 : 256;
   p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
   if (p.slots > p.tiles) p.slots = p.tiles;
   return p;

@@ -605,7 +605,8 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *                [B + 1] int32: prompts; sequence b's tokens are
  *                [cu_seqlens[b], cu_seqlens[b + 1]) and become its last rows, so
  *                kv_len and E count them already.  Tokens of no sequence are
- *                left alone.
+ *                left alone.  From the first sequence at which cu_seqlens
+ *                falls on, sequences have no tokens and SPEC_ST_BAD_STATE.
  *   positions    [T] int32 or NULL: each token's row number
  *   inv_freq     [rot / 2] float32 (NULL if rot is 0); rot even, 0 .. D
  *   q_out        [T, H * G, D] out, contiguous
@@ -628,7 +629,8 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *   out          [B, N, H * G, D] out; lse [B, N, H * G] out or NULL
  *   ws           workspace of spec_tree_attention_workspace_bytes(B, N, H, G,
  *                D, max_rows, dt), max_rows = C, or max_pages * page_size
- *                (contents ignored on entry)
+ *                (contents ignored on entry; calls that may run at the same
+ *                time need one each)
  * A row that sees nothing, or only scores of -inf, gives zeros and an lse of
  * -inf.  Rows that are not seen may hold anything, infinities and NaNs too.
  * Results are the same in every call.  The cache rows are cut over workgroups
@@ -637,7 +639,8 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  * Errors of these calls: SPEC_EINVAL for NULL required pointers, sizes < 1,
  * layer outside [0, L), strides or addresses that are not multiples of 16
  * bytes, scale or eps out of range, outputs that overlap inputs or each other,
- * counts of 2^31 and more; SPEC_ECAPACITY for D > SPEC_ATTN_MAX_D or
+ * counts of 2^31 and more, C or max_pages * page_size above 2^31 - 513;
+ * SPEC_ECAPACITY for D > SPEC_ATTN_MAX_D or
  * N > SPEC_TREE_MAX_N; SPEC_EWORKSPACE.
  * ------------------------------------------------------------------------ */
 int spec_tree_mask(int B, int N, const int32_t *first_child, const int32_t *next_sibling,

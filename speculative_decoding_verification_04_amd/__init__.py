@@ -463,7 +463,7 @@ def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens
     vp, vs, _ = _token_rows(v, H, kv, D, "v", dev, T)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     B = where.shape[0] if paged else planes
-    if cu_seqlens is None and (T % B or not T):
+    if cu_seqlens is None and (B < 1 or T % B or not T):
         raise ValueError(f"{T} tokens are no whole number for each of {B} sequences")
     N = T // B if cu_seqlens is None else 0
     if paged:

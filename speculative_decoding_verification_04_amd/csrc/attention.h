@@ -389,7 +389,9 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
     }
   W.l += sum;
 
-  // O^T += V^T P^T
+  // O^T += V^T P^T.  For the bf16 product the weights are rounded to bf16: off by at
+  // most half a step, 2^-8 of a weight, like the one rounding of the result; their
+  // sum is of the unrounded ones.
   if constexpr (S::kElt == 2) {
 #pragma unroll
     for (int t = 0; t < 2 * S::kNB; ++t) {
@@ -668,7 +670,7 @@ inline int fill(Params &P, const void *q, int64_t q_stride, const void *kv, spec
   const int err = cache_view(P.c, kv, dt, L, planes, H, cols, D, layer, table, max_pages, paged, end_col, kv_len);
   if (err) return err;
   if (B < 1 || G < 1 || (!paged && planes != B)) return SPEC_EINVAL;
-  if (!(scale > 0.0f) || scale > 3.4e38f) return SPEC_EINVAL;
+  if (!(scale > 0.0f) || scale > 2e38f) return SPEC_EINVAL;   // sl stays finite
   if (D > SPEC_ATTN_MAX_D) return SPEC_ECAPACITY;
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return SPEC_EINVAL;
   const int elt = dt == SPEC_BF16 ? 2 : 4;

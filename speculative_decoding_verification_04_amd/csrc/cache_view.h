@@ -36,6 +36,16 @@ __device__ inline int cache_page(const CacheView &c, int r) {
   return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(r)) * c.div_m) >> (31 + c.div_s));
 }
 
+// Packed token ranges [cu[b], cu[b + 1]).  From where cu falls, ranges could hold
+// other sequences' tokens: those sequences have none.  The lane holds sequence
+// b's lo and hi; `fallen` goes from one 64 sequences to the next.
+__device__ inline bool range_follows(bool in, int lo, int hi, bool &fallen) {
+  const uint64_t falls = __ballot(in && lo > hi);
+  const bool before = fallen || (falls & (~0ull >> (kWave - 1 - (threadIdx.x & (kWave - 1)))));   // up to the own
+  fallen |= falls != 0;
+  return !before;
+}
+
 // Bytes from a layer's K (or V) base to column col of (plane, head).
 __device__ inline long long cache_offset(const CacheView &c, int plane, int h, int col, int elt) {
   return ((static_cast<long long>(plane) * c.H + h) * c.cols + col) * c.D * elt;
@@ -54,7 +64,9 @@ inline int cache_view(CacheView &c, const void *kv, spec_dtype dt, int L, int pl
   if (!kv || !kv_len || (paged ? !table : !end_col)) return SPEC_EINVAL;
   if (dt != SPEC_F32 && dt != SPEC_BF16) return SPEC_EINVAL;
   if (L < 1 || planes < 1 || H < 1 || cols < 1 || D < 1 || layer < 0 || layer >= L) return SPEC_EINVAL;
-  if (paged && (max_pages < 1 || static_cast<long long>(max_pages) * cols >= INT32_MAX)) return SPEC_EINVAL;
+  // row numbers, rounded up to whole tiles, stay below 2^31
+  if (paged && max_pages < 1) return SPEC_EINVAL;
+  if ((paged ? static_cast<long long>(max_pages) : 1ll) * cols > INT32_MAX - 512) return SPEC_EINVAL;
   const long long elt = dt == SPEC_BF16 ? 2 : 4;
   const long long half = static_cast<long long>(planes) * H * cols * D * elt;  // one layer's K
   c.k = static_cast<char *>(const_cast<void *>(kv)) + 2 * half * layer;

@@ -102,6 +102,11 @@ __device__ inline void write_status(const RopeParams &P, int b) {
   if (b >= P.B) return;
   const Span s = span_of(P, b, P.cu ? P.cu[b] : 0, P.cu ? P.cu[b + 1] : 0, P.c.kv_len[b], P.c.table ? 0 : *P.c.end_col);
   int st = s.st;
+  if (P.cu) {
+    bool falls = false;                                   // before the sequence
+    for (int i = lane; i < b; i += kWave) falls |= P.cu[i] > P.cu[i + 1];
+    if (__any(falls)) st |= SPEC_ST_BAD_STATE;
+  }
   if (!st && P.c.table && s.len > 0) {
     bool bad = false;
     const int last = cache_page(P.c, s.row0 + s.len - 1);
@@ -172,10 +177,12 @@ __global__ __launch_bounds__(kMaxThreads, 4) void norm_rope_kernel(RopeParams P)
   }
   int b = -1, t0 = 0, t1 = 0, n = 0;
   if (P.cu) {
-    // the first sequence that holds token t
+    // the sequence that holds token t
+    bool fallen = false;
     for (int b0 = 0; b0 < P.B; b0 += kWave) {
       const int i = min(b0 + lane, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1], ni = P.c.kv_len[i];
-      const uint64_t who = __ballot(b0 + lane < P.B && lo <= t && t < hi);
+      const bool follows = range_follows(b0 + lane < P.B, lo, hi, fallen);
+      const uint64_t who = __ballot(b0 + lane < P.B && follows && lo <= t && t < hi);
       if (who) {
         const int l = __ffsll(static_cast<unsigned long long>(who)) - 1;
         b = b0 + l;

@@ -20,10 +20,13 @@ struct Where {
   int b, tile, tiles;
 };
 
-// State of sequence b: its tokens (-1: they are not inside [0, T)) and status.
-__device__ inline int prompt_len(const Params &P, int b) {
-  const int lo = P.cu[b], hi = P.cu[b + 1];
-  return lo >= 0 && lo <= hi && hi <= P.T ? hi - lo : -1;
+// Tokens of the lane's sequence b (b past the last: 0); -1 where its range is not
+// inside [0, T) or does not follow the ones before it.  Whole waves call it, for
+// 64 sequences after the other.
+__device__ inline int prompt_len(const Params &P, int b, bool &fallen) {
+  const int i = min(b, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1];
+  const bool follows = range_follows(b < P.B, lo, hi, fallen);
+  return b >= P.B ? 0 : follows && lo >= 0 && hi <= P.T ? hi - lo : -1;
 }
 __device__ inline int prompt_status(const Params &P, int b, int len) {
   if (len < 0) return SPEC_ST_BAD_STATE;
@@ -50,8 +53,9 @@ __device__ inline int prompt_status(const Params &P, int b, int len) {
 template <int kTileRows>
 __device__ inline Where find_tile(const Params &P, int f) {
   const int lane = threadIdx.x & (kWave - 1);
+  bool fallen = false;
   auto tiles_of = [&](int b) {
-    const int len = b < P.B ? prompt_len(P, b) : 0;
+    const int len = prompt_len(P, b, fallen);
     return len > 0 ? static_cast<int>((static_cast<long long>(len) * P.G + kTileRows - 1) / kTileRows) : 0;
   };
   if (P.B <= kWave && gridDim.x > 512) {
@@ -95,17 +99,18 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
   __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
   const int H = P.c.H;
   const int h = blockIdx.x % H, f = blockIdx.x / H;
-  if (blockIdx.x == 0 && P.status) {
+  if (blockIdx.x == 0 && P.status && threadIdx.x < kWave) {
     // sequences without tokens have no tile that would report on them
-    for (int b = threadIdx.x; b < P.B; b += kThreads) {
-      const int len = prompt_len(P, b);
-      if (len <= 0) P.status[b] = prompt_status(P, b, len);
+    bool fallen = false;
+    for (int b0 = 0; b0 < P.B; b0 += kWave) {
+      const int b = b0 + threadIdx.x, len = prompt_len(P, b, fallen);
+      if (b < P.B && len <= 0) P.status[b] = prompt_status(P, b, len);
     }
   }
   const Where w = find_tile<kTileRows>(P, f);
   if (w.b < 0) return;
   Job J;
-  const int len = prompt_len(P, w.b), st = prompt_status(P, w.b, len), n = P.c.kv_len[w.b];
+  const int len = P.cu[w.b + 1] - P.cu[w.b], st = prompt_status(P, w.b, len), n = P.c.kv_len[w.b];
   J.b = w.b;
   J.h = h;
   J.row0 = w.tile * kTileRows;

@@ -23,9 +23,6 @@ namespace specv {
 namespace {
 using namespace attn;
 
-#ifndef KMIN
-#define KMIN 1
-#endif
 inline int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // How a call is cut: waves side by side, row tiles, pieces aimed at.

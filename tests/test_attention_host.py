@@ -62,10 +62,11 @@ COMMON = [(dict(q=N), sv.SPEC_EINVAL), (dict(kv=N), sv.SPEC_EINVAL), (dict(n=N),
           (dict(qs=257), sv.SPEC_EINVAL), (dict(q=ODD), sv.SPEC_EINVAL), (dict(kv=ODD), sv.SPEC_EINVAL),
           (dict(out=ODD), sv.SPEC_EINVAL), (dict(out=P[0]), sv.SPEC_EINVAL), (dict(out=P[1]), sv.SPEC_EINVAL),
           (dict(st=P[3]), sv.SPEC_EINVAL)]
-SCALES = [(dict(scale=x), sv.SPEC_EINVAL) for x in (0.0, -1.0, float("nan"), float("inf"))]
+SCALES = [(dict(scale=x), sv.SPEC_EINVAL) for x in (0.0, -1.0, float("nan"), float("inf"), 3e38)]
 PAGES = [(dict(table=N), sv.SPEC_EINVAL), (dict(pages=0), sv.SPEC_EINVAL), (dict(page=0), sv.SPEC_EINVAL),
-         (dict(most=0), sv.SPEC_EINVAL), (dict(most=1 << 28), sv.SPEC_EINVAL)]
-RECT = [(dict(E=N), sv.SPEC_EINVAL), (dict(C=0), sv.SPEC_EINVAL)]
+         (dict(most=0), sv.SPEC_EINVAL), (dict(most=1 << 28), sv.SPEC_EINVAL),
+         (dict(most=1, page=2 ** 31 - 512), sv.SPEC_EINVAL)]
+RECT = [(dict(E=N), sv.SPEC_EINVAL), (dict(C=0), sv.SPEC_EINVAL), (dict(C=2 ** 31 - 512), sv.SPEC_EINVAL)]
 
 
 @needs_lib

@@ -174,3 +174,68 @@ def test_graph_replay_and_side_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(kv, want[1])
+
+
+@pytest.mark.parametrize("tail", [0, 70])
+def test_ranges_that_fall_have_no_tokens(tail):
+    """From where cu_seqlens falls on, ranges would hold other sequences' tokens: their caches keep
+    their bits, their status says so, and tokens that only they hold are left alone."""
+    B = 4 + tail
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(20, 4, 64, generator=gen).to(DEV)
+    kv, out = torch.zeros(1, 2, B, 1, 16, 64, device=DEV), torch.full((20, 2, 64), 3.0, device=DEV)
+    st = torch.full((B,), -7, dtype=torch.int32, device=DEV)
+    n = i32([10] * B)
+    note(f"norm rope falling ranges tail={tail}")
+    sv.spec_norm_rope_kv(x[:, :2], x[:, 2:3], x[:, 3:], kv, 0, i32([12]), n, out, status=st,
+                         cu_seqlens=i32([0, 8, 2, 6, 15] + [15] * tail))
+    assert st.cpu().tolist() == [0] + [sv.SPEC_ST_BAD_STATE] * (B - 1)
+    assert torch.equal(out[:8], x[:8, :2]) and bool((out[8:] == 3.0).all())
+    assert torch.equal(kv[0, 0, 0, 0, 4:12], x[:8, 2]) and torch.equal(kv[0, 1, 0, 0, 4:12], x[:8, 3])
+    assert float(kv[:, :, 1:].abs().max()) == 0.0 and float(kv[:, :, 0, :, :4].abs().max()) == 0.0
+    if tail:                                               # a fall among the first 64 is known behind them
+        cu = [0, 8, 2] + [2] * 60 + [2 + i for i in range(B - 62)]
+        out.fill_(3.0)
+        kv.zero_()
+        sv.spec_norm_rope_kv(x[:, :2], x[:, 2:3], x[:, 3:], kv, 0, i32([12]), n, out, status=st, cu_seqlens=i32(cu))
+        assert st.cpu().tolist() == [0] + [sv.SPEC_ST_BAD_STATE] * (B - 1)
+        assert bool((out[8:] == 3.0).all()) and float(kv[:, :, 1:].abs().max()) == 0.0
+
+
+def test_no_sequences_and_no_tokens_are_refused():
+    x = torch.zeros(2, 4, 64, device=DEV)
+    empty = torch.zeros(1, 2, 0, 1, 16, 64, device=DEV)
+    kv = torch.zeros(1, 2, 1, 1, 16, 64, device=DEV)
+    z = i32([0])
+    note("norm rope nothing")
+    with pytest.raises(ValueError):
+        sv.spec_norm_rope_kv(x[:, :2], x[:, 2:3], x[:, 3:], empty, 0, z, z, torch.zeros(2, 2, 64, device=DEV))
+    with pytest.raises(ValueError):
+        sv.spec_norm_rope_kv(x[:0, :2], x[:0, 2:3], x[:0, 3:], kv, 0, z, z, torch.zeros(0, 2, 64, device=DEV))
+
+
+def test_graph_replay_into_pages():
+    rng = np.random.default_rng(9)
+    x, w = dev(randn(rng, "f32", 9, 6, 64)), dev(randn(rng, "f32", 64))
+    pool = torch.zeros(2, 2, 8, 1, 4, 64, device=DEV)
+    out, st = torch.empty(9, 4, 64, device=DEV), torch.full((2,), -7, dtype=torch.int32, device=DEV)
+    table, n, cu = i32([[5, 1, 0], [2, 7, 3]]), i32([10, 6]), i32([0, 4, 9])
+    f = torch.from_numpy(_freq(16)).to(DEV)
+    call = lambda: sv.spec_norm_rope_kv_paged(x[:, :4], x[:, 4:5], x[:, 5:], pool, 1, table, n, out,  # noqa: E731
+                                              cu_seqlens=cu, q_weight=w, inv_freq=f, interleaved=True, status=st)
+    note("norm rope paged graph")
+    call()
+    torch.cuda.synchronize()
+    want = out.clone(), pool.clone()
+    assert st.cpu().tolist() == [0, 0] and float(pool[0].abs().max()) == 0.0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        out.zero_()
+        pool.zero_()
+        st.fill_(-7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(pool, want[1]) and st.cpu().tolist() == [0, 0]
+        call()

@@ -156,3 +156,65 @@ def test_graph_replay_and_side_stream():
         call()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("H,G,tail", [(2, 2, 0), (32, 8, 0), (2, 2, 70)])
+def test_ranges_that_fall_have_no_tokens(H, G, tail):
+    """From where cu_seqlens falls on, ranges would hold other sequences' tokens: no sequence there has any,
+    and those before it are served.  With 32 heads the grid exceeds the chip; tail: more than 64 sequences."""
+    rng = np.random.default_rng(14)
+    lens = np.array([60, 0, 5, 90] + [1] * tail)
+    cache = Cache(rng, "bf16", 1, H, 64, lens, lens)
+    q, kv = dev(randn(rng, "bf16", 150, H * G, 64)), dev(cache.kv)
+    note(f"prompt attention falling ranges H={H} tail={tail}")
+    good, _, st = _call(q, cache, kv, 0, [0, 60, 60, 65, 65] + [65] * tail, [60, 0, 5, 90] + [1] * tail)
+    assert st.cpu().tolist() == [0] * (4 + tail)
+    out, l, st = _call(q, cache, kv, 0, [0, 60, 30, 35, 125] + [125] * tail, lens)
+    bad = sv.SPEC_ST_BAD_STATE
+    assert st.cpu().tolist() == [0] + [bad] * (3 + tail)
+    assert torch.equal(out[:60], good[:60]) and bool((out[60:] == 7.0).all()) and bool((l[60:] == 7.0).all())
+    # all of the tokens twice: no workgroup is missing
+    out, _, st = _call(q, cache, kv, 0, [0, 60, 60, 0, 60] + [60] * tail, lens)
+    assert st.cpu().tolist() == [0, 0] + [bad] * (2 + tail)
+    assert torch.equal(out[:60], good[:60]) and bool((out[60:] == 7.0).all())
+
+
+def test_equal_and_empty_prompts_in_a_grid_past_the_chip():
+    """Many sequences of equal and of no length, in a grid that exceeds the chip."""
+    _check(15, "bf16", [130, 0, 130, 64, 1, 0, 130], 16, 8, 64, 16)
+
+
+def test_two_graphs_and_two_streams_on_the_rectangle():
+    rng = np.random.default_rng(16)
+    lens = np.array([33, 150])
+    c = Cache(rng, "f32", 2, 2, 128, lens, lens)
+    kv, cu, E, n = dev(c.kv), i32([0, 33, 183]), c.where(), i32(lens)
+    qs = [dev(randn(rng, "f32", 183, 6, 128)) for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    call = lambda i, s=None: sv.spec_prompt_attention(qs[i], kv, i, cu, E, n, outs[i], stream=s)  # noqa: E731
+    note("prompt attention two graphs")
+    for i in (0, 1):
+        call(i)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        call(i, sides[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs = []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append(g)
+    for rep in range(3):
+        for i in (0, 1):
+            outs[i].zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        call(rep % 2)

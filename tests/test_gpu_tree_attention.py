@@ -287,3 +287,63 @@ def test_repeated_calls_streams_and_graphs_sharing_a_workspace():
         call(rep % 2)
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_more_sequences_than_lanes():
+    rng = np.random.default_rng(61)
+    _check(62, "bf16", rng.integers(0, 300, 130), 3, 1, 4, 64, 16, "tree")
+    _check(63, "f32", rng.integers(0, 200, 70), 2, 2, 2, 64, 0, "chain")
+    n = rng.integers(1, 150, 100)
+    cache = Cache(rng, "bf16", 1, 2, 64, n + 1, n)
+    q, kv = dev(randn(rng, "bf16", 100, 4, 64)).view(100, 1, 4, 64), dev(cache.kv)
+    good, _, _ = _call(q, cache, kv, 0, n, None, 100, 1)
+    wrong = n.copy()
+    wrong[[0, 64, 99]] = -1, cache.E + 1, -2 ** 31
+    note("tree attention bad states of many sequences")
+    out, l, st = _call(q, cache, kv, 0, wrong, None, 100, 1)
+    ok = np.setdiff1d(np.arange(100), [0, 64, 99])
+    assert [b for b in range(100) if st[b].item()] == [0, 64, 99]
+    assert _near(out[ok], good[ok])
+    assert float(out[[0, 64, 99]].float().abs().max()) == 0.0 and bool((l[[0, 64, 99]] == -np.inf).all())
+
+
+def test_graph_over_pages_and_two_streams_at_once():
+    """Two calls at the same time, each with its workspace, and a graph whose lengths change between replays."""
+    rng = np.random.default_rng(71)
+    N, H, G, D = 5, 2, 7, 128
+    most = np.array([900, 333])
+    c = Cache(rng, "bf16", 2, H, D, most + N, most, 16)
+    kv, table, code = dev(c.kv), c.where(), sv.SPEC_BF16
+    need = sv.spec_tree_attention_workspace_bytes(2, N, H, G, D, c.max_rows(), code)
+    ws = [torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    qs = [dev(randn(rng, "bf16", 2 * N, H * G, D)).view(2, N, H * G, D) for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    lens = [i32([900, 333]), i32([17, 200])]
+    n = lens[0].clone()
+    call = lambda i, s=None: sv.spec_tree_attention_paged(qs[i], kv, i, table, n, outs[i], ws[i], stream=s)  # noqa: E731
+    note("tree attention two streams")
+    want = []
+    for x in lens:
+        n.copy_(x)
+        for i in (0, 1):
+            call(i)
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        call(i, sides[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want[1]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(0)
+    for rep in range(4):
+        n.copy_(lens[rep % 2])
+        outs[0].zero_()
+        g.replay()
+        call(1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want[rep % 2]))

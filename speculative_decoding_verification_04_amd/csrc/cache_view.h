@@ -36,16 +36,6 @@ __device__ inline int cache_page(const CacheView &c, int r) {
   return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(r)) * c.div_m) >> (31 + c.div_s));
 }
 
-// Packed token ranges [cu[b], cu[b + 1]).  From where cu falls, ranges could hold
-// other sequences' tokens: those sequences have none.  The lane holds sequence
-// b's lo and hi; `fallen` goes from one 64 sequences to the next.
-__device__ inline bool range_follows(bool in, int lo, int hi, bool &fallen) {
-  const uint64_t falls = __ballot(in && lo > hi);
-  const bool before = fallen || (falls & (~0ull >> (kWave - 1 - (threadIdx.x & (kWave - 1)))));   // up to the own
-  fallen |= falls != 0;
-  return !before;
-}
-
 // Bytes from a layer's K (or V) base to column col of (plane, head).
 __device__ inline long long cache_offset(const CacheView &c, int plane, int h, int col, int elt) {
   return ((static_cast<long long>(plane) * c.H + h) * c.cols + col) * c.D * elt;

@@ -21,11 +21,13 @@ struct Where {
 };
 
 // Tokens of the lane's sequence b (b past the last: 0); -1 where its range is not
-// inside [0, T) or does not follow the ones before it.  Whole waves call it, for
-// 64 sequences after the other.
+// inside [0, T), or where cu falls there or before: it could hold other sequences'
+// tokens.  Whole waves call it, for 64 sequences after the other.
 __device__ inline int prompt_len(const Params &P, int b, bool &fallen) {
   const int i = min(b, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1];
-  const bool follows = range_follows(b < P.B, lo, hi, fallen);
+  const uint64_t falls = __ballot(b < P.B && lo > hi);
+  const bool follows = !fallen && !(falls & (~0ull >> (kWave - 1 - (threadIdx.x & (kWave - 1)))));   // up to the own
+  fallen |= falls != 0;
   return b >= P.B ? 0 : follows && lo >= 0 && hi <= P.T ? hi - lo : -1;
 }
 __device__ inline int prompt_status(const Params &P, int b, int len) {

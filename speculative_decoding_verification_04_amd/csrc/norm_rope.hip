@@ -346,6 +346,14 @@ int norm_rope_call(const void *q, int64_t q_stride, const void *k, int64_t k_str
   const int elt = dt == SPEC_BF16 ? 2 : 4, Hq = H * G;
   if (static_cast<long long>(H) * (G + 2) >= INT32_MAX / D || static_cast<long long>(T) + B >= INT32_MAX)
     return SPEC_EINVAL;
+  P.lanes = 1;
+  while (P.lanes * (16 / elt) < D) P.lanes *= 2;
+  // one token's heads, in whole waves
+  const long long lanes = static_cast<long long>(H) * (G + 2) * P.lanes;
+  const int threads = static_cast<int>(lanes < kMaxThreads ? round_up(lanes, kWave) : kMaxThreads);
+  const int waves = threads / kWave;
+  const unsigned grid = static_cast<unsigned>(T) + (status ? (static_cast<long long>(B) + waves - 1) / waves : 0);
+  if (!launchable(grid, threads)) return SPEC_EINVAL;
   const long long qh = static_cast<long long>(Hq) * D, kh = static_cast<long long>(H) * D;
   if (D * elt % 16 || q_stride < qh || k_stride < kh || v_stride < kh) return SPEC_EINVAL;
   if (q_stride * elt % 16 || k_stride * elt % 16 || v_stride * elt % 16) return SPEC_EINVAL;
@@ -380,8 +388,6 @@ int norm_rope_call(const void *q, int64_t q_stride, const void *k, int64_t k_str
   P.N = N;
   P.Hq = Hq;
   P.half = rot / 2;
-  P.lanes = 1;
-  while (P.lanes * (16 / elt) < D) P.lanes *= 2;
   P.cu = cu;
   P.positions = positions;
   P.q_weight = q_weight;
@@ -389,11 +395,6 @@ int norm_rope_call(const void *q, int64_t q_stride, const void *k, int64_t k_str
   P.eps = eps;
   P.inv_freq = inv_freq;
   P.status = status;
-  // one token's heads, in whole waves
-  const long long lanes = static_cast<long long>(H) * (G + 2) * P.lanes;
-  const int threads = static_cast<int>(lanes < kMaxThreads ? round_up(lanes, kWave) : kMaxThreads);
-  const int waves = threads / kWave;
-  const unsigned grid = static_cast<unsigned>(T) + (status ? (B + waves - 1) / waves : 0);
   (void)hipGetLastError();
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int n = 16 / elt, apart = P.half / n;

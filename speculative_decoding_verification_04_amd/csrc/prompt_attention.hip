@@ -150,7 +150,10 @@ inline long long prompt_grid(int T, int B, int H, int G, int rw) {
 
 template <typename T, int DP, int RW>
 int launch_rows(const Params &P, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(prompt_grid(P.T, P.B, P.c.H, P.G, RW)));
+  const long long workgroups = prompt_grid(P.T, P.B, P.c.H, P.G, RW);
+  if (!launchable(workgroups, kThreads)) return SPEC_EINVAL;
+  const dim3 grid(static_cast<unsigned>(workgroups));
+  (void)hipGetLastError();
   if (P.c.table)
     hipLaunchKernelGGL((prompt_kernel<T, DP, RW, true>), grid, dim3(kThreads), 0, s, P);
   else
@@ -181,7 +184,7 @@ int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, 
                        kv_len, scale, out, lse, status);
   if (err) return err;
   if (T < 1) return SPEC_EINVAL;
-  if (static_cast<long long>(T) * G >= INT32_MAX || prompt_grid(T, B, H, G, 2) >= INT32_MAX) return SPEC_EINVAL;
+  if (static_cast<long long>(T) * G >= INT32_MAX) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const void *ins[] = {q, kv, table, end_col, kv_len, cu};
   const size_t in_n[] = {((T - 1) * static_cast<size_t>(q_stride) + hd) * elt, cache_bytes(dt, L, planes, H, cols, D),
@@ -197,7 +200,6 @@ int prompt_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, 
   P.T = T;
   P.cu = cu;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  (void)hipGetLastError();
   if (dt == SPEC_BF16)
     return D <= 64 ? launch_prompt<__bf16, 64>(P, s)
                    : D <= 128 ? launch_prompt<__bf16, 128>(P, s) : launch_prompt<__bf16, 256>(P, s);

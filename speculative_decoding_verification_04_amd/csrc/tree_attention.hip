@@ -30,6 +30,9 @@ using namespace attn;
 
 inline int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
+// Workgroups that join `rows` query rows: a wave each.
+inline long long join_grid(long long rows) { return (rows + kThreads / kWave - 1) / (kThreads / kWave); }
+
 // How a call is cut: waves side by side, row tiles, pieces aimed at.
 struct Plan {
   int rw, kt, row_tiles, target;
@@ -51,6 +54,11 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
   if (p.slots > p.tiles) p.slots = p.tiles;
   return p;
+}
+
+// Both launches fit, and the kernel's sums of tiles (with a target added) stay below 2^31.
+inline bool plan_fits(const Plan &p, long long rows) {
+  return p.tiles <= INT32_MAX - p.target && launchable(p.slots, kThreads) && launchable(join_grid(rows), kThreads);
 }
 
 // Workspace: a slot for each piece, and each group's pieces.
@@ -292,8 +300,8 @@ int launch_both(const Params &P, const Plan &p, hipStream_t s) {
   launch_tree<T, DP>(P, p, s);
   const int st = launch_status();
   if (st != SPEC_OK) return st;
-  const int waves = kThreads / kWave, rows = P.B * P.c.H * P.N * P.G;
-  hipLaunchKernelGGL((join_kernel<T, DP>), dim3((rows + waves - 1) / waves), dim3(kThreads), 0, s, P, 32 * p.rw);
+  const unsigned joins = static_cast<unsigned>(join_grid(static_cast<long long>(P.B) * P.c.H * P.N * P.G));
+  hipLaunchKernelGGL((join_kernel<T, DP>), dim3(joins), dim3(kThreads), 0, s, P, 32 * p.rw);
   return launch_status();
 }
 
@@ -314,10 +322,10 @@ int tree_call(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, in
   if (N < 1) return SPEC_EINVAL;
   if (N > SPEC_TREE_MAX_N) return SPEC_ECAPACITY;
   if (!aligned(mask, 4)) return SPEC_EINVAL;
-  const long long tokens = static_cast<long long>(B) * N;
-  if (tokens * H * G >= INT32_MAX) return SPEC_EINVAL;
+  const long long tokens = static_cast<long long>(B) * N, rows = tokens * H * G;
+  if (rows >= INT32_MAX) return SPEC_EINVAL;
   const Plan p = plan_of(B, N, H, G, D, cache_capacity(P.c), dt);
-  if (p.tiles >= INT32_MAX || p.slots >= INT32_MAX) return SPEC_EINVAL;
+  if (!plan_fits(p, rows)) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const int words = (N + 31) / 32;
   const Space sp = space_of(p, D);
@@ -359,8 +367,10 @@ extern "C" size_t spec_tree_attention_workspace_bytes(int B, int N, int H, int G
   if (B < 1 || N < 1 || N > SPEC_TREE_MAX_N || H < 1 || G < 1 || D < 1 || D > SPEC_ATTN_MAX_D || max_rows < 1) return 0;
   if (dt != SPEC_F32 && dt != SPEC_BF16) return 0;
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return 0;
-  if (static_cast<long long>(B) * N * H * G >= INT32_MAX) return 0;
-  return space_of(plan_of(B, N, H, G, D, max_rows, dt), D).end;
+  const long long rows = static_cast<long long>(B) * N * H * G;
+  if (rows >= INT32_MAX) return 0;
+  const Plan p = plan_of(B, N, H, G, D, max_rows, dt);
+  return plan_fits(p, rows) ? space_of(p, D).end : 0;
 }
 
 extern "C" int spec_tree_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B, int H,

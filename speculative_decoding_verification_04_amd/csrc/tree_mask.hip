@@ -12,7 +12,7 @@
 // ancestor at distance 2^t), so a chain of 255 links takes 8 rounds and not
 // 255.  Bound by its barriers and LDS round trips: one tree of 16 nodes 2.5 us, 256
 // trees of 255 nodes 6.5 us (2.9 MB read and written).
-#include "common.h"
+#include "cache_view.h"
 
 namespace specv {
 namespace {
@@ -125,6 +125,8 @@ extern "C" int spec_tree_mask(int B, int N, const int32_t *first_child, const in
   if (!first_child || !next_sibling || !kv_len || !positions || !mask) return SPEC_EINVAL;
   if (B < 1 || N < 1) return SPEC_EINVAL;
   if (N > SPEC_TREE_MAX_N) return SPEC_ECAPACITY;
+  const int threads = static_cast<int>(round_up(N, kWave));
+  if (!launchable(B, threads)) return SPEC_EINVAL;
   const int words = (N + 31) / 32;
   const size_t b4 = static_cast<size_t>(B) * 4, bn4 = b4 * N;
   const void *ins[] = {first_child, next_sibling, kv_len};
@@ -140,6 +142,6 @@ extern "C" int spec_tree_mask(int B, int N, const int32_t *first_child, const in
   }
   TreeMaskParams P{N, words, first_child, next_sibling, kv_len, positions, mask, status};
   (void)hipGetLastError();
-  hipLaunchKernelGGL(tree_mask_kernel, dim3(B), dim3(static_cast<unsigned>(round_up(N, kWave))), 0, static_cast<hipStream_t>(stream), P);
+  hipLaunchKernelGGL(tree_mask_kernel, dim3(B), dim3(threads), 0, static_cast<hipStream_t>(stream), P);
   return launch_status();
 }

@@ -177,3 +177,59 @@ def test_binding_checks_rows():
                       ((t[::2], torch.int32, 4, "kv_len", -1), "must be contiguous")]:
         with pytest.raises(ValueError, match=why):
             sv._need(*args)
+
+
+# addresses 16 TB apart, so that sizes near the limits do not overlap
+FAR = [ctypes.c_void_p((i + 1) << 44) for i in range(9)]
+
+
+@needs_lib
+@pytest.mark.parametrize("B,N", [(1 << 24, 256), (1 << 25, 65), (1 << 26, 1), (2 ** 31 - 1, 64)])
+def test_tree_mask_refuses_launches_past_32_bits(B, N):
+    assert LIB.spec_tree_mask(B, N, *FAR[:5], None, None) == sv.SPEC_EINVAL
+
+
+@needs_lib
+@pytest.mark.parametrize("T,G,st", [(1 << 24, 254, N), (1 << 26, 1, N), ((1 << 24) - 1, 254, FAR[8])])
+def test_rope_refuses_launches_past_32_bits(T, G, st):
+    """A workgroup of 64 lanes (3 heads of one lane each) or 256 (256 heads) a token, and some for the status."""
+    big = dict(q=FAR[0], qs=8 * G, k=FAR[1], ks=8, v=FAR[2], vs=8, kv=FAR[3], H=1, D=8, rot=8, G=G, T=T, out=FAR[5])
+    assert LIB.spec_norm_rope_kv(*_args(ROPE, **big, B=1, N=T, C=64, E=FAR[6], n=FAR[7], f=FAR[4], st=st)) == sv.SPEC_EINVAL
+    assert LIB.spec_norm_rope_kv_paged(*_args(ROPE_P, **big, B=1, N=T, table=FAR[6], n=FAR[7], f=FAR[4], st=st)) == sv.SPEC_EINVAL
+
+
+@needs_lib
+@pytest.mark.parametrize("B,T,H", [(1 << 24, 5, 1), (1 << 20, 5, 16), (1, (2 ** 31 - 2) // 2, 2)])
+def test_prompts_refuse_launches_past_32_bits(B, T, H):
+    big = dict(q=FAR[0], qs=16 * H, kv=FAR[1], L=1, layer=0, H=H, D=8, T=T, n=FAR[3], cu=FAR[4], out=FAR[5], B=B)
+    assert LIB.spec_prompt_attention(*_args(PROMPT, **big, C=8, E=FAR[2])) == sv.SPEC_EINVAL
+    assert LIB.spec_prompt_attention_paged(*_args(PROMPT_P, **big, table=FAR[2], most=1)) == sv.SPEC_EINVAL
+
+
+@needs_lib
+@pytest.mark.parametrize("B,nodes,H,G", [(1 << 10, 256, 1, 256), (1 << 25, 1, 1, 2), (1 << 24, 1, 1, 1), (1 << 20, 2, 16, 1)])
+def test_trees_refuse_launches_past_32_bits(B, nodes, H, G):
+    """2^26 query rows need 2^32 lanes to join; 2^24 pieces as many to attend.  The workspace query says 0."""
+    assert sv.spec_tree_attention_workspace_bytes(B, nodes, H, G, 8, 512, sv.SPEC_BF16) == 0
+    big = dict(q=FAR[0], qs=8 * H * G, kv=FAR[1], L=1, layer=0, H=H, D=8, N=nodes, G=G, n=FAR[3], out=FAR[4], B=B,
+               ws=FAR[5], wsb=1 << 43)
+    assert LIB.spec_tree_attention(*_args(TREE, **big, C=512, E=FAR[2])) == sv.SPEC_EINVAL
+    assert LIB.spec_tree_attention_paged(*_args(TREE_P, **big, table=FAR[2], most=32)) == sv.SPEC_EINVAL
+
+
+@needs_lib
+def test_the_largest_tree_calls_that_fit():
+    """Just below: the query names a size, and the checks end at the workspace (its size is not enough)."""
+    assert sv.spec_tree_attention_workspace_bytes((1 << 10) - 1, 256, 1, 256, 8, 512, sv.SPEC_BF16) > 0
+    big = dict(q=FAR[0], qs=8 * 256, kv=FAR[1], L=1, layer=0, H=1, D=8, N=256, G=256, n=FAR[3], out=FAR[4],
+               B=(1 << 10) - 1, ws=FAR[5], wsb=256)
+    assert LIB.spec_tree_attention(*_args(TREE, **big, C=512, E=FAR[2])) == sv.SPEC_EWORKSPACE
+
+
+@needs_lib
+def test_tile_counts_stay_below_31_bits_with_the_target_added():
+    big = dict(q=FAR[0], qs=8, kv=FAR[1], L=1, layer=0, H=1, D=8, N=1, G=1, n=FAR[3], out=FAR[4], ws=FAR[5], wsb=1 << 43)
+    tiles = (2 ** 31 - 100) // 129                        # of 128 rows: 129 sequences have 2^31 - 137, a target is 256
+    for each, code in [(tiles, sv.SPEC_EINVAL), (tiles - 2, sv.SPEC_EWORKSPACE)]:
+        args = dict(big, wsb=256, B=129, table=FAR[2], most=each * 8, pages=9, page=16)
+        assert LIB.spec_tree_attention_paged(*_args(TREE_P, **args)) == code

@@ -606,7 +606,9 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *                [cu_seqlens[b], cu_seqlens[b + 1]) and become its last rows, so
  *                kv_len and E count them already.  Tokens of no sequence are
  *                left alone.  From the first sequence at which cu_seqlens
- *                falls on, sequences have no tokens and SPEC_ST_BAD_STATE.
+ *                falls on, sequences have no tokens and SPEC_ST_BAD_STATE; one
+ *                whose range reaches past [0, T] has that status too, and
+ *                those of its tokens that are in [0, T).
  *   positions    [T] int32 or NULL: each token's row number
  *   inv_freq     [rot / 2] float32 (NULL if rot is 0); rot even, 0 .. D
  *   q_out        [T, H * G, D] out, contiguous

@@ -27,7 +27,7 @@ struct Where {
 };
 
 // Tokens of the lane's sequence b (b past the last: 0); -1 where its range is not
-// inside [0, T), or where cu falls there or before: it could hold other sequences'
+// inside [0, T], or where cu falls there or before: it could hold other sequences'
 // tokens.  Whole waves call it, for 64 sequences after the other.
 __device__ inline int prompt_len(const Params &P, int b, bool &fallen) {
   const int i = min(b, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1];
@@ -51,7 +51,8 @@ __device__ inline int prompt_status(const Params &P, int b, int len) {
   return st;
 }
 
-// The sequence and tile of flat tile number f; b = -1 past the last.
+// The sequence and tile of flat tile number f.  Past the last: b = -1, the number
+// among those that have no tile, and how many they are.
 // Where the workgroups do not all fit the chip at once, up to 64 sequences' tiles
 // are taken by their number, the highest (the longest walks) of all sequences
 // first, so that no long walk starts late: 8 prompts of 256 .. 2048 tokens (14
@@ -71,7 +72,7 @@ __device__ inline Where find_tile(const Params &P, int f) {
     auto from = [&](int level) {
       return wave_reduce(max(0, tiles - level), [](int x, int y) { return x + y; });
     };
-    if (from(0) <= f) return Where{-1, 0, 0};
+    if (from(0) <= f) return Where{-1, f - from(0), static_cast<int>(gridDim.x / P.c.H) - from(0)};
     int lo = 0, hi = wave_max_i(tiles);                   // from(lo) > f >= from(hi) = 0
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -96,7 +97,33 @@ __device__ inline Where find_tile(const Params &P, int f) {
     }
     base += read_lane(upto, kWave - 1);
   }
-  return Where{-1, 0, 0};
+  return Where{-1, f - base, static_cast<int>(gridDim.x / P.c.H) - base};
+}
+
+// A range that reaches past the call's tokens has no tiles, and its sequence a
+// status; the tokens that it does have get zeros, from the workgroups without a
+// tile (the grid counts at least one for each such sequence): workgroup `which`
+// of `of`.
+template <typename T>
+__device__ inline void zero_outside(const Params &P, long long which, long long of) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const long long heads = static_cast<long long>(P.c.H) * P.G, row = heads * P.c.D * sizeof(T) / 16;
+  for (int b0 = 0; b0 < P.B; b0 += kWave) {
+    const int i = min(b0 + lane, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1];
+    const bool is = b0 + lane < P.B;
+    const uint64_t falls = __ballot(is && lo > hi);       // no tokens from there on
+    uint64_t outside = __ballot(is && (lo < 0 || hi > P.T));
+    if (falls) outside &= (falls & -falls) - 1;
+    for (; outside; outside &= outside - 1) {
+      const int l = __ffsll(static_cast<unsigned long long>(outside)) - 1;
+      const long long t0 = max(read_lane(lo, l), 0), t1 = min(read_lane(hi, l), P.T);
+      u32x4 *out = reinterpret_cast<u32x4 *>(P.out);
+      for (long long x = t0 * row + which * kThreads + threadIdx.x; x < t1 * row; x += of * kThreads) out[x] = u32x4{0, 0, 0, 0};
+      if (P.lse)
+        for (long long x = t0 * heads + which * kThreads + threadIdx.x; x < t1 * heads; x += of * kThreads) P.lse[x] = -INFINITY;
+    }
+    if (falls) return;
+  }
 }
 
 template <typename T, int DP, int RW, bool PAGED>
@@ -116,7 +143,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
     }
   }
   const Where w = find_tile<kTileRows>(P, f);
-  if (w.b < 0) return;
+  if (w.b < 0) {
+    zero_outside<T>(P, static_cast<long long>(w.tile) * H + h, static_cast<long long>(w.tiles) * H);
+    return;
+  }
   Job J;
   const int len = P.cu[w.b + 1] - P.cu[w.b], st = prompt_status(P, w.b, len), n = P.c.kv_len[w.b];
   J.b = w.b;

@@ -412,8 +412,8 @@ def spec_tree_mask(first_child, next_sibling, kv_len, positions, mask, *, status
     """first_child, next_sibling [B, N], kv_len [B] int32; positions [B, N] int32 out, mask
     [B, N, ceil(N / 32)] int32 out (bit words), for spec_norm_rope_kv and spec_tree_attention."""
     B, N = first_child.shape
-    i32 = torch.int32
     dev, s = _place(first_child, stream)
+    i32 = torch.int32
     code = library().spec_tree_mask(
         B, N, _need(first_child, i32, B * N, "first_child", dev), _need(next_sibling, i32, B * N, "next_sibling", dev),
         _need(kv_len, i32, B, "kv_len", dev), _need(positions, i32, B * N, "positions", dev),

@@ -40,3 +40,21 @@ def test_the_package_and_its_build_import_without_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.split() == ["256", "True", "SpecError"], r.stderr
+
+
+@pytest.mark.parametrize("call", ["mask", "rope", "rope_paged", "prompt", "prompt_paged", "tree", "tree_paged", "dtype"])
+def test_any_call_may_be_the_first(call, monkeypatch):
+    """No call reads a name that only an earlier call would have bound."""
+    for name in ("torch", "_current_device", "_raw_stream"):
+        monkeypatch.setattr(sv, name, None)
+    kv, q, i = torch.zeros(1, 2, 2, 2, 8, 64), torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, dtype=torch.int32)
+    run = {"mask": lambda: sv.spec_tree_mask(i, i, i, i, i),
+           "rope": lambda: sv.spec_norm_rope_kv(q, q[:, :, :2], q[:, :, :2], kv, 0, i, i, q),
+           "rope_paged": lambda: sv.spec_norm_rope_kv_paged(q, q[:, :, :2], q[:, :, :2], kv, 0, i, i, q),
+           "prompt": lambda: sv.spec_prompt_attention(q[0], kv, 0, i, i, i, q[0]),
+           "prompt_paged": lambda: sv.spec_prompt_attention_paged(q[0], kv, 0, i, i, i, q[0]),
+           "tree": lambda: sv.spec_tree_attention(q, kv, 0, i, i, q, i),
+           "tree_paged": lambda: sv.spec_tree_attention_paged(q, kv, 0, i, i, q, i),
+           "dtype": lambda: sv._dtype_code(i)}[call]
+    with pytest.raises(ValueError, match="must be on the GPU|unsupported dtype"):
+        run()

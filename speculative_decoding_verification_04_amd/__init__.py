@@ -575,15 +575,16 @@ def _tree(name, paged, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, s
     _check(code, name)
 
 
-def spec_tree_attention(q, kv, layer: int, end_col, kv_len, out, ws=None, *, mask=None, scale=None, lse=None,
+def spec_tree_attention(q, kv, layer: int, end_col, kv_len, out, ws, *, mask=None, scale=None, lse=None,
                         status=None, stream=None) -> None:
     """Attention of q [B, N, H * G, D] (the verify forward's nodes, their slots already at columns
     E .. E + N - 1 of kv [L, 2, B, H, C, D]) over the cached rows and each node's visible nodes;
-    mask [B, N, ceil(N / 32)] int32 as from spec_tree_mask, None: a chain.  out [B, N, H * G, D]."""
+    mask [B, N, ceil(N / 32)] int32 as from spec_tree_mask, None: a chain.  out [B, N, H * G, D].
+    ws: workspace(spec_tree_attention_workspace_bytes(...)), as in every call that takes one."""
     _tree("spec_tree_attention", False, q, kv, layer, end_col, kv_len, out, ws, mask, scale, lse, status, stream)
 
 
-def spec_tree_attention_paged(q, pool, layer: int, block_table, kv_len, out, ws=None, *, mask=None, scale=None,
+def spec_tree_attention_paged(q, pool, layer: int, block_table, kv_len, out, ws, *, mask=None, scale=None,
                               lse=None, status=None, stream=None) -> None:
     """spec_tree_attention over a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages]."""
     _tree("spec_tree_attention_paged", True, q, pool, layer, block_table, kv_len, out, ws, mask, scale, lse, status,

@@ -1,6 +1,7 @@
 """Host-side argument checks of the Python binding (no GPU): dtype, size and
 device are checked before a pointer reaches the C library, which cannot check
 them itself."""
+import inspect
 import os
 import subprocess
 import sys
@@ -58,3 +59,9 @@ def test_any_call_may_be_the_first(call, monkeypatch):
            "dtype": lambda: sv._dtype_code(i)}[call]
     with pytest.raises(ValueError, match="must be on the GPU|unsupported dtype"):
         run()
+
+
+@pytest.mark.parametrize("f", [sv.spec_tree_attention, sv.spec_tree_attention_paged])
+def test_tree_attention_asks_for_its_workspace(f):
+    """A default could only fail: the call cannot run without one."""
+    assert inspect.signature(f).parameters["ws"].default is inspect.Parameter.empty

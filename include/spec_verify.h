@@ -573,8 +573,13 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *                not written, except that rows on good pages may be; their
  *                attention output is zero, or unspecified where a page id is
  *                bad.  Other sequences are not affected.
- * No call takes a gradient; bf16 results are float32 results rounded once.
- * Sums, maxima and statistics are float32.
+ * No call takes a gradient.  Scores, maxima, sums and statistics are float32,
+ * and results are rounded to dt once, at the store.  One rounding stands before
+ * it, in the attention calls over bf16 caches only: the softmax weights
+ * exp(s - m) are rounded to bf16 for the product with V (their sum is of the
+ * unrounded ones), each by at most half a step, 2^-8 of it, so an element may
+ * be off by 2^-8 sum_j P_j |v_j| (P: the weights over their sum) beside its own
+ * rounding.  Over float32 caches weights stay float32.
  *
  * spec_tree_mask -- positions and visibility of a tree's nodes, once per round
  * for all layers.

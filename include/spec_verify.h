@@ -640,9 +640,13 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *                time need one each)
  * A row that sees nothing, or only scores of -inf, gives zeros and an lse of
  * -inf.  Rows that are not seen may hold anything, infinities and NaNs too.
- * Results are the same in every call.  The cache rows are cut over workgroups
- * by the lengths of the whole batch, so a sequence's result may differ by
- * rounding between batches of other lengths.
+ * Both attention calls: results are the same bits whenever a call is repeated.
+ * Between batches a sequence's result may differ by the order of its sums:
+ * spec_tree_attention cuts the cache rows over workgroups by the lengths of all
+ * sequences, and spec_prompt_attention gives a workgroup 64 or 128 query rows by
+ * T * G * H.  Where the same bits are needed whatever else runs, call the
+ * sequence alone (in the paged forms with B = 1 and its row of the block table):
+ * then only its own lengths count.
  * Errors of these calls: SPEC_EINVAL for NULL required pointers, sizes < 1,
  * layer outside [0, L), strides or addresses that are not multiples of 16
  * bytes, scale or eps out of range, outputs that overlap inputs or each other,

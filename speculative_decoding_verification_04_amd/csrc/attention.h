@@ -84,21 +84,18 @@ struct Shape {
   static_assert(kLoads * kThreads == kKT * kChunks && (kKW == 1 || 2 * kJoins >= kKW) && 2 * kLds <= 160 * 1024 - 2048, "LDS");
 };
 
-// LDS place of chunk c of row r.  Rows of 256 bytes and more all start at bank
-// 0, so the chunk is exchanged by the row: four rows side by side (the block
-// that a transposing read of V takes) get four different pairs of chunks, and
-// sixteen rows (a read of K) sixteen different chunks.  Rows of 128 bytes
-// start at two places, and eight chunks serve two rows each.
+// Chunk c of row r lies at LDS place r * CHUNKS + (c ^ turn(r)).  Rows of 256
+// bytes and more all start at bank 0, so the chunk is exchanged by the row: four
+// rows side by side (the block that a transposing read of V takes) get four
+// different pairs of chunks, and sixteen rows (a read of K) sixteen different
+// chunks.  Rows of 128 bytes start at two places, and eight chunks serve two rows
+// each.
 template <int CHUNKS>
 __device__ inline int turn(int r) {
   if constexpr (CHUNKS >= 16)
     return ((r & 3) << 2) | ((r >> 2) & 3);
   else
     return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-}
-template <int CHUNKS>
-__device__ inline int place(int r, int c) {
-  return r * CHUNKS + (c ^ turn<CHUNKS>(r));
 }
 
 __device__ inline float half_max(float x) {
@@ -464,8 +461,10 @@ __device__ inline void put4(char *out, int d0, int D, const float (&x)[4]) {
   }
 }
 
-// The walk of one job.  The waves kw == 0 return with their rows' unscaled
-// outputs, maxima and sums; all return whether a bad page was met.
+// The walk of one job.  Each wave returns with its share of its rows' unscaled
+// outputs (of KW waves on the same rows the kw-th has the kw-th DP / KW
+// elements) and with the rows' maxima and sums over all of them; all return
+// whether a bad page was met.
 template <typename T, int DP, int RW, bool PAGED, bool PROMPT, bool ONCE>
 __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP, RW>::kKW> &D, char *buf0,
                             char *buf1) {

@@ -9,8 +9,10 @@
 // of its KV head, which fit one workgroup's tile (32, 64 or 128 rows) unless
 // the tree and the group are large.  With one workgroup per (sequence, KV
 // head, row tile) a batch does not fill the chip, so each such group's cache
-// rows are cut into pieces of about the same length, whatever the sequences'
-// lengths, which the workgroups find on the device; the pieces' partial results
+// rows are cut into pieces of at most a common length, which the workgroups find
+// on the device from the sequences' lengths (a group's own pieces differ by a
+// tile at most; groups of other lengths have others: trees over 25k and 33k rows
+// get pieces of 98 or 99 and of 129 tiles); the pieces' partial results
 // go to the workspace and a second launch joins them, in the order of the
 // pieces, one wave for each query row.  (Joining them in the first launch, by
 // the workgroup that brings a group's last piece, took 19 us instead of 16 for
@@ -49,7 +51,10 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   p.row_tiles = static_cast<int>((R + 32 * p.rw - 1) / (32 * p.rw));
   p.groups = static_cast<long long>(B) * H * p.row_tiles;
   p.tiles = p.groups * ((max_rows + p.kt - 1) / p.kt);
-  // what the chip holds at once: two workgroups a CU where LDS and registers allow
+  // A piece for each workgroup that the chip holds at once, one a CU, or two where
+  // a row takes up to 256 bytes and a workgroup more than 32 query rows.  (512 for
+  // all: 66-node float32 trees, 28 heads of 128, took 46 us instead of 37.)  The
+  // kernels of bf16 heads up to 64 would fit once more on a CU than this counts.
   p.target = p.rw > 1 && row <= 256 ? 512 : 256;
   p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
   if (p.slots > p.tiles) p.slots = p.tiles;
@@ -111,7 +116,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
   // Tiles of a piece, at most: so many that the pieces fit the chip at once.  A
   // few workgroups more than that would run alone behind all the others: 16-node
   // trees over 32 sequences of 512 .. 4096 rows took 74 us so and 84 us without
-  // the second look, 255-node trees over 32k rows 324 and 410 us.
+  // the second look, 255-node trees over 32k rows 324 and 410 us.  It is not taken
+  // for more than 64 sequences, nor where the groups alone exceed the target.
   int per = max(1, (total + P.target - 1) / P.target);
   if (P.B <= kWave && each * P.B <= P.target)
     while (per > 1 && wave_reduce((tiles0 + per - 1) / per, [](int a, int c) { return a + c; }) * each > P.target)

@@ -76,20 +76,21 @@ __device__ inline Span span_of(const RopeParams &P, int b, int t0, int t1, int n
   Span s;
   s.st = 0;
   if (P.cu) {
-    s.t0 = t0;
-    s.len = t1 - t0;
-    if (t0 < 0 || s.len < 0 || t1 > P.T) s.st = SPEC_ST_BAD_STATE;
-    s.row0 = n - s.len;
-    if (s.row0 < 0) s.st |= SPEC_ST_BAD_STATE;
+    // no difference is taken before its operands are known to be in range
+    const bool in = t0 >= 0 && t0 <= t1 && t1 <= P.T;
+    s.t0 = in ? t0 : 0;
+    s.len = in ? t1 - t0 : 0;
+    if (!in || n < s.len) s.st = SPEC_ST_BAD_STATE;
+    s.row0 = s.st ? 0 : n - s.len;
   } else {
     s.t0 = b * P.N;
     s.len = P.N;
     s.row0 = n;
     if (n < 0) s.st = SPEC_ST_BAD_STATE;
   }
-  const long long cap = cache_capacity(P.c);
+  const long long cap = cache_capacity(P.c), end = static_cast<long long>(n) + (P.cu ? 0 : P.N);
   if (P.c.table) {
-    if (static_cast<long long>(s.row0) + s.len > cap) s.st |= SPEC_ST_CAPACITY;
+    if (end > cap) s.st |= SPEC_ST_CAPACITY;
   } else {
     if (E < 0 || static_cast<long long>(E) + (P.cu ? 0 : P.N) > cap) s.st |= SPEC_ST_CAPACITY;
     if (n > E) s.st |= SPEC_ST_BAD_STATE;

@@ -239,3 +239,29 @@ def test_graph_replay_into_pages():
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(pool, want[1]) and st.cpu().tolist() == [0, 0]
         call()
+
+
+@pytest.mark.parametrize("page", [0, 4])
+@pytest.mark.parametrize("E", [2, 12])                    # below and above the prompt's length
+def test_lengths_at_the_ends_of_the_range(page, E):
+    """Lengths whose difference from a prompt's leaves 32 bits are out of range like any others: a status, and
+    a cache that keeps its bits; and so are ranges at the ends of theirs."""
+    low, high = -2 ** 31, 2 ** 31 - 1
+    bad, full = sv.SPEC_ST_BAD_STATE, sv.SPEC_ST_CAPACITY
+    x = torch.randn(15, 4, 64, generator=torch.Generator().manual_seed(3)).to(DEV)
+    for n, cu, want in [([low, low + 4, low], [0, 5, 10, 15], [bad] * 3), ([low, -1, 4], [0, 5, 10, 15], [bad] * 3),
+                        ([high, 5, 5], [0, 0, 0, 0], [full if page else bad] + [0 if page or E > 5 else bad] * 2),
+                        ([low, low, low], [low, 5, 15, high], [bad] * 3), ([0, 0, 5], [0, 0, low, 5], [0, bad, bad])]:
+        kv = torch.zeros(1, 2, 3, 1, 16, 64, device=DEV)
+        pool = torch.zeros(1, 2, 12, 1, 4, 64, device=DEV)
+        out, st = torch.zeros(15, 2, 64, device=DEV), torch.full((3,), -7, dtype=torch.int32, device=DEV)
+        more = dict(cu_seqlens=i32(cu), status=st)
+        note(f"norm rope ends of the range page={page} E={E} n={n} cu={cu}")
+        if page:
+            sv.spec_norm_rope_kv_paged(x[:, :2], x[:, 2:3], x[:, 3:], pool, 0, i32(np.arange(12).reshape(3, 4)), i32(n),
+                                       out, **more)
+        else:
+            sv.spec_norm_rope_kv(x[:, :2], x[:, 2:3], x[:, 3:], kv, 0, i32([E]), i32(n), out, **more)
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == want, (n, cu)
+        assert float(kv.abs().max()) == 0.0 and float(pool.abs().max()) == 0.0

@@ -636,8 +636,8 @@ int spec_group_same_length(const int32_t *lengths, int N, int B, int min_group,
  *   out          [B, N, H * G, D] out; lse [B, N, H * G] out or NULL
  *   ws           workspace of spec_tree_attention_workspace_bytes(B, N, H, G,
  *                D, max_rows, dt), max_rows = C, or max_pages * page_size
- *                (contents ignored on entry; calls that may run at the same
- *                time need one each)
+ *                (0 for sizes that the call refuses; contents ignored on
+ *                entry; calls that may run at the same time need one each)
  * A row that sees nothing, or only scores of -inf, gives zeros and an lse of
  * -inf.  Rows that are not seen may hold anything, infinities and NaNs too.
  * Both attention calls: results are the same bits whenever a call is repeated.

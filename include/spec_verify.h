@@ -695,6 +695,120 @@ int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool,
                               const uint32_t *mask, float scale, void *out, float *lse, int32_t *status,
                               void *ws, size_t ws_bytes, spec_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * The attention half on a cache held in 4 bits.
+ * Batch decoding is bound by reading the cache; here an element takes 4.25 bits.
+ * A row (D elements of one layer, K or V, plane, head and column) is D / 2 bytes of
+ * codes and D / 32 bytes of scales, in two arrays of the cache's layout:
+ *   codes   [L][2][B][H][C][D / 2], or [L][2][pages][H][page_size][D / 2]
+ *   scales  [L][2][B][H][C][D / 32], or [L][2][pages][H][page_size][D / 32]
+ * Code (4 bits; the even element of a pair in the low half of its byte): a sign
+ * (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1).  Scale of each 32 elements: a
+ * power of two as its exponent + 127; a byte above 252 stands for 32 NaNs.  An
+ * element is its code's value times its scale, which bf16 and float32 hold exactly
+ * (byte 0, which no call writes, counts as byte 1).
+ * The rows' bytes are whole elements of bf16, so the calls that move rows take both
+ * arrays as bf16 caches, one after the other: codes with D / 4 for D, scales with
+ * D / 64 (spec_commit_realign_kv, spec_resync_draft_kv, spec_repad_kv,
+ * spec_unpad_kv, spec_compact_tree_kv, spec_compact_tree_paged).
+ *
+ * Arguments, status bits, results and errors are those of the calls above without
+ * _mx, with these differences:
+ *   dt           the type of q, k, v, weights and outputs; the cache has none
+ *   D            a multiple of 64, at most SPEC_ATTN_MAX_D
+ *   codes, scales  multiples of 16 bytes; they may not overlap each other
+ *
+ * spec_norm_rope_kv_mx -- as spec_norm_rope_kv; keys (computed in float64 from
+ * their inputs, so that which code an element gets is a matter of its value and not
+ * of roundings) and values become codes.  With a the largest magnitude of 32
+ * elements, the scale is 2^e with e = floor(log2 a) - 2, one more where
+ * a >= 1.75 * 2^floor(log2 a), and -125 <= e <= 125; an element x gets the code
+ * nearest to x / 2^e, the even one of two, at most 6.  32 elements of which one is
+ * not finite, as float32, get the scale byte 255 and codes of 0.
+ *
+ * spec_unpack_kv_mx -- rows as their values: the rows that spec_norm_rope_kv_mx
+ * writes for the same T, N, cu_seqlens, kv_len and end_col or block_table, token by
+ * token.
+ *   k_out, v_out [T, H, D] of dt out, multiples of 16 bytes.  Rows of sequences with
+ *                a status, and rows on bad pages, give zeros (of a range that
+ *                reaches past [0, T], the tokens in [0, T) do); tokens of no sequence
+ *                are left alone.
+ *
+ * spec_prompt_attention_mx, spec_tree_attention_mx -- the attention calls, with
+ * keys and values as the cache's codes stand for.  Over dt bf16 softmax weights are
+ * rounded to bf16 for the product with V, as over bf16 caches; dt float32 keeps
+ * float32.  ws: spec_tree_attention_mx_workspace_bytes(B, N, H, G, D, max_rows, dt).
+ *
+ * spec_compact_tree_paged -- spec_compact_tree_kv over pages, for caches of any
+ * kind: the tree forward wrote node i of sequence b as row n_b + i; rows
+ * n_b + path[b, 0 .. e_b - 1] become, in order and in place, rows n_b .. n_b + e_b - 1
+ * of every layer, K/V and head, after which spec_commit_paged(k = N - 1) commits.
+ *   pool         [L][2][pages][H][page_size][D] of dt, element-aligned
+ *   block_table  [B, max_pages] int32; kv_len [B] n_b
+ *   path [B, N], emit_count [B]  as from the tree verification
+ *   status       [B] out or NULL: SPEC_ST_BAD_STATE for n_b < 0, e_b outside
+ *                [0, N], a path that does not start at 0 and rise inside the tree, or
+ *                a page id outside [0, pages) under a kept slot or its new place;
+ *                SPEC_ST_CAPACITY where rows n_b + N do not fit the table.  Such a
+ *                sequence is left unchanged.
+ * Pages that hold rows from n_b on belong to one sequence; where two share one, or a
+ * table names one twice, the rows there are unspecified.
+ * Errors: SPEC_EINVAL for NULL required pointers, sizes < 1, misalignment, overlap,
+ * max_pages * page_size above 2^31 - 513, counts of 2^31 and more, more than
+ * 2^32 - 1 work-items (256 for each sequence, layer, K/V and, where those are fewer
+ * than 2048, group of heads); SPEC_ECAPACITY for N > SPEC_TREE_MAX_N.
+ * ------------------------------------------------------------------------ */
+int spec_norm_rope_kv_mx(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, uint8_t *codes, uint8_t *scales, spec_dtype dt, int L, int B,
+                         int H, int C, int D, int layer, int T, int N, int G, const int32_t *end_col,
+                         const int32_t *kv_len, const int32_t *cu_seqlens, const int32_t *positions,
+                         const void *q_weight, const void *k_weight, float eps, const float *inv_freq,
+                         int rot, int interleaved, void *q_out, int32_t *status, spec_stream_t stream);
+int spec_norm_rope_kv_mx_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, uint8_t *codes, uint8_t *scales,
+                               spec_dtype dt, int L, int pages, int H, int page_size, int D, int layer,
+                               int T, int B, int N, int G, const int32_t *block_table, int max_pages,
+                               const int32_t *kv_len, const int32_t *cu_seqlens, const int32_t *positions,
+                               const void *q_weight, const void *k_weight, float eps,
+                               const float *inv_freq, int rot, int interleaved, void *q_out,
+                               int32_t *status, spec_stream_t stream);
+int spec_unpack_kv_mx(const uint8_t *codes, const uint8_t *scales, spec_dtype dt, int L, int B, int H, int C,
+                      int D, int layer, int T, int N, const int32_t *end_col, const int32_t *kv_len,
+                      const int32_t *cu_seqlens, void *k_out, void *v_out, int32_t *status,
+                      spec_stream_t stream);
+int spec_unpack_kv_mx_paged(const uint8_t *codes, const uint8_t *scales, spec_dtype dt, int L, int pages,
+                            int H, int page_size, int D, int layer, int T, int B, int N,
+                            const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                            const int32_t *cu_seqlens, void *k_out, void *v_out, int32_t *status,
+                            spec_stream_t stream);
+int spec_prompt_attention_mx(const void *q, int64_t q_stride, const uint8_t *codes, const uint8_t *scales,
+                             spec_dtype dt, int L, int B, int H, int C, int D, int layer, int T, int G,
+                             const int32_t *end_col, const int32_t *kv_len, const int32_t *cu_seqlens,
+                             float scale, void *out, float *lse, int32_t *status, spec_stream_t stream);
+int spec_prompt_attention_mx_paged(const void *q, int64_t q_stride, const uint8_t *codes,
+                                   const uint8_t *scales, spec_dtype dt, int L, int pages, int H,
+                                   int page_size, int D, int layer, int B, int T, int G,
+                                   const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                                   const int32_t *cu_seqlens, float scale, void *out, float *lse,
+                                   int32_t *status, spec_stream_t stream);
+size_t spec_tree_attention_mx_workspace_bytes(int B, int N, int H, int G, int D, int max_rows,
+                                              spec_dtype dt);
+int spec_tree_attention_mx(const void *q, int64_t q_stride, const uint8_t *codes, const uint8_t *scales,
+                           spec_dtype dt, int L, int B, int H, int C, int D, int layer, int N, int G,
+                           const int32_t *end_col, const int32_t *kv_len, const uint32_t *mask, float scale,
+                           void *out, float *lse, int32_t *status, void *ws, size_t ws_bytes,
+                           spec_stream_t stream);
+int spec_tree_attention_mx_paged(const void *q, int64_t q_stride, const uint8_t *codes, const uint8_t *scales,
+                                 spec_dtype dt, int L, int pages, int H, int page_size, int D, int layer,
+                                 int B, int N, int G, const int32_t *block_table, int max_pages,
+                                 const int32_t *kv_len, const uint32_t *mask, float scale, void *out,
+                                 float *lse, int32_t *status, void *ws, size_t ws_bytes,
+                                 spec_stream_t stream);
+int spec_compact_tree_paged(void *pool, spec_dtype dt, int L, int pages, int H, int page_size, int D, int B,
+                            int N, const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                            const int32_t *path, const int32_t *emit_count, int32_t *status,
+                            spec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,7 +39,7 @@ from .process import process_row, process_rows, sample_verify_logits  # noqa: F4
 from .realign import commit_bookkeeping, position_and_mask, commit_realign, resync_draft  # noqa: F401
 from .group import group_same_length  # noqa: F401
 from .paged import commit_paged  # noqa: F401
-from .tree import tree_verify, compact_tree_slots  # noqa: F401
+from .tree import tree_verify, compact_tree_slots, compact_tree_pages  # noqa: F401
 from .tree_sample import tree_sample_verify  # noqa: F401
 from .unbatched import UnbatchedModel, check_ragged  # noqa: F401
 from .ragged import repad_kv, unpad_kv, ragged_bytes  # noqa: F401
@@ -47,3 +47,4 @@ from .policy import eqspec_round, exspec_round  # noqa: F401
 from .attention import (  # noqa: F401
     tree_paths, mask_words, norm_rope, row_places, cache_rows, attend,
 )
+from . import mx  # noqa: F401

@@ -103,6 +103,18 @@ def compact_tree_slots(kv, E: int, path, emit_count) -> np.ndarray:
     return new
 
 
+def compact_tree_pages(pool, table, n, path, emit_count) -> np.ndarray:
+    """Copy of pool [L, 2, pages, H, page, D] where each sequence's kept tree
+    rows (row n + path[b, j] of its pages) are moved to rows n + j, j < emit_count[b]."""
+    new = pool.copy()
+    page = pool.shape[4]
+    for b in range(len(n)):
+        for j in range(int(emit_count[b])):
+            to, of = int(n[b]) + j, int(n[b]) + int(path[b, j])
+            new[:, :, table[b, to // page], :, to % page] = pool[:, :, table[b, of // page], :, of % page]
+    return new
+
+
 def chain_links(B: int, N: int):
     """first_child / next_sibling of a linear chain 0 -> 1 -> ... -> N-1."""
     fc = np.full((B, N), -1, np.int32)

@@ -30,6 +30,9 @@ __all__ = [
     "spec_tree_mask", "spec_norm_rope_kv", "spec_norm_rope_kv_paged", "spec_prompt_attention",
     "spec_prompt_attention_paged", "spec_tree_attention_workspace_bytes", "spec_tree_attention",
     "spec_tree_attention_paged", "SPEC_ATTN_MAX_D",
+    "spec_norm_rope_kv_mx", "spec_norm_rope_kv_mx_paged", "spec_unpack_kv_mx", "spec_unpack_kv_mx_paged",
+    "spec_prompt_attention_mx", "spec_prompt_attention_mx_paged", "spec_tree_attention_mx_workspace_bytes",
+    "spec_tree_attention_mx", "spec_tree_attention_mx_paged", "spec_compact_tree_paged",
     "spec_group_same_length", "workspace", "library",
 ]
 
@@ -421,11 +424,11 @@ def spec_tree_mask(first_child, next_sibling, kv_len, positions, mask, *, status
     _check(code, "spec_tree_mask")
 
 
-def _token_rows(t, heads: int, kv, D: int, name: str, dev: int, tokens: int = 0):
-    """Address, token stride (elements) and count of [..., heads, D] rows of the cache's dtype: contiguous
+def _token_rows(t, heads: int, ref, D: int, name: str, dev: int, tokens: int = 0):
+    """Address, token stride (elements) and count of [..., heads, D] rows of ref's dtype: contiguous
     heads, one stride from token to token (a view of a fused projection will do)."""
-    if t.dtype is not kv.dtype:
-        raise ValueError(f"{name} must be {kv.dtype}, not {t.dtype}")
+    if t.dtype is not ref.dtype:
+        raise ValueError(f"{name} must be {ref.dtype}, not {t.dtype}")
     shape, step = t.shape, t.stride()
     if len(shape) not in (3, 4) or shape[-2] != heads or shape[-1] != D:
         raise ValueError(f"{name} must be [..., {heads}, {D}], got {tuple(shape)}")
@@ -466,14 +469,33 @@ def _same_size(out, ref, count: int, name: str, dev: int):
     return _need(out, ref.dtype, count, name, dev)
 
 
-def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
-               inv_freq, interleaved, status, stream):
-    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2])
+def _mx_dims(codes, scales, heads: int):
+    """As _cache_dims, of a cache of 4-bit numbers: codes [L, 2, planes, H, cols, D / 2] and scales
+    [L, 2, planes, H, cols, D / 32], uint8."""
+    L, planes, H, cols, half, G = _cache_dims(codes, heads)
+    if tuple(scales.shape) != tuple(codes.shape[:5]) + (half // 16,) or half % 32:
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)}: D / 2 and D / 32 of a D that "
+                         "is a multiple of 64 are needed")
+    return L, planes, H, cols, 2 * half, G
+
+
+def _cache_at(kv, scales, heads: int, stream):
+    """A call's cache: its sizes as _cache_dims gives them, its device and stream, and its address, or those
+    of a cache of 4-bit numbers' codes and scales."""
+    dims = _cache_dims(kv, heads) if scales is None else _mx_dims(kv, scales, heads)
     dev, s = _place(kv, stream)
-    i32 = torch.int32
-    qp, qs, T = _token_rows(q, H * G, kv, D, "q", dev)
-    kp, ks, _ = _token_rows(k, H, kv, D, "k", dev, T)
-    vp, vs, _ = _token_rows(v, H, kv, D, "v", dev, T)
+    if scales is None:
+        return dims, dev, s, (kv.data_ptr(),)
+    return dims, dev, s, (_need(kv, torch.uint8, 0, "codes", dev), _need(scales, torch.uint8, 0, "scales", dev))
+
+
+def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
+               inv_freq, interleaved, status, stream, scales=None):
+    (L, planes, H, cols, D, G), dev, s, cache = _cache_at(kv, scales, q.shape[-2], stream)
+    i32, ref = torch.int32, kv if scales is None else q     # ref: of the call's dtype
+    qp, qs, T = _token_rows(q, H * G, ref, D, "q", dev)
+    kp, ks, _ = _token_rows(k, H, ref, D, "k", dev, T)
+    vp, vs, _ = _token_rows(v, H, ref, D, "v", dev, T)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     B = where.shape[0] if paged else planes
     if cu_seqlens is None and (B < 1 or T % B or not T):
@@ -483,15 +505,14 @@ def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens
         sizes = (planes, H, cols, D, int(layer), T, B, N, G, _need(where, i32, B, "block_table", dev), where.shape[1])
     else:
         sizes = (planes, H, cols, D, int(layer), T, N, G, _need(where, i32, 1, "end_col", dev))
-    dt = kv.dtype
     code = getattr(library(), name)(
-        qp, qs, kp, ks, vp, vs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        qp, qs, kp, ks, vp, vs, *cache, _dtype_code(q), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
         None if cu_seqlens is None else _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev),
         None if positions is None else _need(positions, i32, T, "positions", dev),
-        None if q_weight is None else _need(q_weight, dt, D, "q_weight", dev),
-        None if k_weight is None else _need(k_weight, dt, D, "k_weight", dev),
+        None if q_weight is None else _need(q_weight, ref.dtype, D, "q_weight", dev),
+        None if k_weight is None else _need(k_weight, ref.dtype, D, "k_weight", dev),
         eps, _need(inv_freq, torch.float32, 0, "inv_freq", dev) if rot else None, rot, 1 if interleaved else 0,
-        _same_size(q_out, kv, T * H * G * D, "q_out", dev), _need(status, i32, B, "status", dev, True), s)
+        _same_size(q_out, ref, T * H * G * D, "q_out", dev), _need(status, i32, B, "status", dev, True), s)
     _check(code, name)
 
 
@@ -513,11 +534,10 @@ def spec_norm_rope_kv_paged(q, k, v, pool, layer: int, block_table, kv_len, q_ou
                positions, q_weight, k_weight, eps, inv_freq, interleaved, status, stream)
 
 
-def _prompt(name, paged, q, kv, layer, cu_seqlens, where, kv_len, out, scale, lse, status, stream):
-    L, planes, H, cols, D, G = _cache_dims(kv, q.shape[-2])
-    dev, s = _place(kv, stream)
-    i32 = torch.int32
-    qp, qs, T = _token_rows(q, H * G, kv, D, "q", dev)
+def _prompt(name, paged, q, kv, layer, cu_seqlens, where, kv_len, out, scale, lse, status, stream, scales=None):
+    (L, planes, H, cols, D, G), dev, s, cache = _cache_at(kv, scales, q.shape[-2], stream)
+    i32, ref = torch.int32, kv if scales is None else q     # ref: of the call's dtype
+    qp, qs, T = _token_rows(q, H * G, ref, D, "q", dev)
     if paged:
         B = where.shape[0]
         sizes = (planes, H, cols, D, int(layer), B, T, G, _need(where, i32, B, "block_table", dev), where.shape[1])
@@ -525,9 +545,9 @@ def _prompt(name, paged, q, kv, layer, cu_seqlens, where, kv_len, out, scale, ls
         B = planes
         sizes = (B, H, cols, D, int(layer), T, G, _need(where, i32, 1, "end_col", dev))
     code = getattr(library(), name)(
-        qp, qs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        qp, qs, *cache, _dtype_code(q), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
         _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev), D ** -0.5 if scale is None else scale,
-        _same_size(out, kv, T * H * G * D, "out", dev), _need(lse, torch.float32, T * H * G, "lse", dev, True),
+        _same_size(out, ref, T * H * G * D, "out", dev), _need(lse, torch.float32, T * H * G, "lse", dev, True),
         _need(status, i32, B, "status", dev, True), s)
     _check(code, name)
 
@@ -552,14 +572,13 @@ def spec_tree_attention_workspace_bytes(B: int, N: int, H: int, G: int, D: int, 
     return int(library().spec_tree_attention_workspace_bytes(B, N, H, G, D, max_rows, dtype_code))
 
 
-def _tree(name, paged, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, status, stream):
+def _tree(name, paged, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, status, stream, scales=None):
     if q.dim() != 4:
         raise ValueError(f"q must be [B, N, heads, D], got {tuple(q.shape)}")
     B, N, heads, _ = q.shape
-    L, planes, H, cols, D, G = _cache_dims(kv, heads)
-    dev, s = _place(kv, stream)
-    i32 = torch.int32
-    qp, qs, T = _token_rows(q, heads, kv, D, "q", dev)
+    (L, planes, H, cols, D, G), dev, s, cache = _cache_at(kv, scales, heads, stream)
+    i32, ref = torch.int32, kv if scales is None else q     # ref: of the call's dtype
+    qp, qs, T = _token_rows(q, heads, ref, D, "q", dev)
     if (where.shape[0] if paged else planes) != B:
         raise ValueError(f"q has {B} sequences, the cache {where.shape[0] if paged else planes}")
     if paged:
@@ -567,9 +586,9 @@ def _tree(name, paged, q, kv, layer, where, kv_len, out, ws, mask, scale, lse, s
     else:
         sizes = (B, H, cols, D, int(layer), N, G, _need(where, i32, 1, "end_col", dev))
     code = getattr(library(), name)(
-        qp, qs, kv.data_ptr(), _dtype_code(kv), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        qp, qs, *cache, _dtype_code(q), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
         _need(mask, i32, T * ((N + 31) // 32), "mask", dev, True), D ** -0.5 if scale is None else scale,
-        _same_size(out, kv, T * heads * D, "out", dev), _need(lse, torch.float32, T * heads, "lse", dev, True),
+        _same_size(out, ref, T * heads * D, "out", dev), _need(lse, torch.float32, T * heads, "lse", dev, True),
         _need(status, i32, B, "status", dev, True), None if ws is None else _need(ws, ws.dtype, 0, "ws", dev),
         0 if ws is None else ws.numel() * ws.element_size(), s)
     _check(code, name)
@@ -589,3 +608,110 @@ def spec_tree_attention_paged(q, pool, layer: int, block_table, kv_len, out, ws,
     """spec_tree_attention over a page pool [L, 2, pages, H, page_size, D]; block_table [B, max_pages]."""
     _tree("spec_tree_attention_paged", True, q, pool, layer, block_table, kv_len, out, ws, mask, scale, lse, status,
           stream)
+
+
+def spec_norm_rope_kv_mx(q, k, v, codes, scales, layer: int, end_col, kv_len, q_out, *, cu_seqlens=None,
+                         positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                         interleaved: bool = False, status=None, stream=None) -> None:
+    """spec_norm_rope_kv into a cache of 4-bit numbers: codes [L, 2, B, H, C, D / 2] and scales
+    [L, 2, B, H, C, D / 32], uint8; D a multiple of 64."""
+    _norm_rope("spec_norm_rope_kv_mx", False, q, k, v, codes, layer, end_col, kv_len, q_out, cu_seqlens, positions,
+               q_weight, k_weight, eps, inv_freq, interleaved, status, stream, scales)
+
+
+def spec_norm_rope_kv_mx_paged(q, k, v, codes, scales, layer: int, block_table, kv_len, q_out, *, cu_seqlens=None,
+                               positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                               interleaved: bool = False, status=None, stream=None) -> None:
+    """spec_norm_rope_kv_mx into pages: codes [L, 2, pages, H, page_size, D / 2], scales [..., D / 32];
+    block_table [B, max_pages] int32."""
+    _norm_rope("spec_norm_rope_kv_mx_paged", True, q, k, v, codes, layer, block_table, kv_len, q_out, cu_seqlens,
+               positions, q_weight, k_weight, eps, inv_freq, interleaved, status, stream, scales)
+
+
+def _unpack(name, paged, codes, scales, layer, where, kv_len, k_out, v_out, cu_seqlens, status, stream):
+    (L, planes, H, cols, D, _), dev, s, cache = _cache_at(codes, scales, codes.shape[3], stream)
+    i32 = torch.int32
+    B = where.shape[0] if paged else planes
+    if k_out.numel() % (H * D) or not k_out.numel():
+        raise ValueError(f"k_out must hold [T, {H}, {D}] elements, has {k_out.numel()}")
+    T = k_out.numel() // (H * D)
+    if cu_seqlens is None and (B < 1 or T % B):
+        raise ValueError(f"{T} tokens are no whole number for each of {B} sequences")
+    N = T // B if cu_seqlens is None else 0
+    if paged:
+        sizes = (planes, H, cols, D, int(layer), T, B, N, _need(where, i32, B, "block_table", dev), where.shape[1])
+    else:
+        sizes = (planes, H, cols, D, int(layer), T, N, _need(where, i32, 1, "end_col", dev))
+    code = getattr(library(), name)(
+        *cache, _dtype_code(k_out), L, *sizes, _need(kv_len, i32, B, "kv_len", dev),
+        None if cu_seqlens is None else _need(cu_seqlens, i32, B + 1, "cu_seqlens", dev),
+        _need(k_out, k_out.dtype, T * H * D, "k_out", dev), _same_size(v_out, k_out, T * H * D, "v_out", dev),
+        _need(status, i32, B, "status", dev, True), s)
+    _check(code, name)
+
+
+def spec_unpack_kv_mx(codes, scales, layer: int, end_col, kv_len, k_out, v_out, *, cu_seqlens=None, status=None,
+                      stream=None) -> None:
+    """Rows of a cache of 4-bit numbers as their values, k_out, v_out [T, H, D] (bf16 / f32): those that
+    spec_norm_rope_kv_mx writes for T tokens with the same kv_len, end_col and cu_seqlens."""
+    _unpack("spec_unpack_kv_mx", False, codes, scales, layer, end_col, kv_len, k_out, v_out, cu_seqlens, status, stream)
+
+
+def spec_unpack_kv_mx_paged(codes, scales, layer: int, block_table, kv_len, k_out, v_out, *, cu_seqlens=None,
+                            status=None, stream=None) -> None:
+    """spec_unpack_kv_mx from pages; block_table [B, max_pages] int32."""
+    _unpack("spec_unpack_kv_mx_paged", True, codes, scales, layer, block_table, kv_len, k_out, v_out, cu_seqlens,
+            status, stream)
+
+
+def spec_prompt_attention_mx(q, codes, scales, layer: int, cu_seqlens, end_col, kv_len, out, *, scale=None, lse=None,
+                             status=None, stream=None) -> None:
+    """spec_prompt_attention over a cache of 4-bit numbers; q and out share a dtype (bf16 / f32)."""
+    _prompt("spec_prompt_attention_mx", False, q, codes, layer, cu_seqlens, end_col, kv_len, out, scale, lse, status,
+            stream, scales)
+
+
+def spec_prompt_attention_mx_paged(q, codes, scales, layer: int, cu_seqlens, block_table, kv_len, out, *, scale=None,
+                                   lse=None, status=None, stream=None) -> None:
+    """spec_prompt_attention_paged over a cache of 4-bit numbers."""
+    _prompt("spec_prompt_attention_mx_paged", True, q, codes, layer, cu_seqlens, block_table, kv_len, out, scale, lse,
+            status, stream, scales)
+
+
+def spec_tree_attention_mx_workspace_bytes(B: int, N: int, H: int, G: int, D: int, max_rows: int,
+                                           dtype_code: int) -> int:
+    """max_rows: C of the rectangle, or max_pages * page_size; dtype_code: of q and out."""
+    return int(library().spec_tree_attention_mx_workspace_bytes(B, N, H, G, D, max_rows, dtype_code))
+
+
+def spec_tree_attention_mx(q, codes, scales, layer: int, end_col, kv_len, out, ws, *, mask=None, scale=None, lse=None,
+                           status=None, stream=None) -> None:
+    """spec_tree_attention over a cache of 4-bit numbers; q and out share a dtype (bf16 / f32).
+    ws: workspace(spec_tree_attention_mx_workspace_bytes(...))."""
+    _tree("spec_tree_attention_mx", False, q, codes, layer, end_col, kv_len, out, ws, mask, scale, lse, status, stream,
+          scales)
+
+
+def spec_tree_attention_mx_paged(q, codes, scales, layer: int, block_table, kv_len, out, ws, *, mask=None, scale=None,
+                                 lse=None, status=None, stream=None) -> None:
+    """spec_tree_attention_paged over a cache of 4-bit numbers."""
+    _tree("spec_tree_attention_mx_paged", True, q, codes, layer, block_table, kv_len, out, ws, mask, scale, lse,
+          status, stream, scales)
+
+
+def spec_compact_tree_paged(pool, block_table, kv_len, path, emit_count, *, status=None, stream=None) -> None:
+    """pool [L, 2, pages, H, page_size, D] (bf16/f32), block_table [B, max_pages], kv_len [B], path [B, N] and
+    emit_count [B] int32: rows n + path[b, 0 .. e-1] moved together to n .. n + e - 1 in place.  A cache of
+    4-bit numbers: codes.view(torch.bfloat16), then scales.view(torch.bfloat16)."""
+    if pool.dim() != 6 or pool.shape[1] != 2:
+        raise ValueError("pool must be [L, 2, pages, H, page_size, D]")
+    L, _, pages, H, page_size, D = pool.shape
+    (B, max_pages), N = block_table.shape, path.shape[-1]
+    dev, s = _place(pool, stream)
+    i32 = torch.int32
+    code = library().spec_compact_tree_paged(
+        _need(pool, pool.dtype, 0, "pool", dev), _dtype_code(pool), L, pages, H, page_size, D, B, N,
+        _need(block_table, i32, B, "block_table", dev), max_pages, _need(kv_len, i32, B, "kv_len", dev),
+        _need(path, i32, B * N, "path", dev), _need(emit_count, i32, B, "emit_count", dev),
+        _need(status, i32, B, "status", dev, True), s)
+    _check(code, "spec_compact_tree_paged")

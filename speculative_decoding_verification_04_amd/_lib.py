@@ -56,6 +56,22 @@ PROTOTYPES = {
     "spec_tree_attention_paged": (_I, [_P, _S, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _F, _P,
                                        _P, _P, _P, _SZ, _P]),
     "spec_group_same_length": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "spec_norm_rope_kv_mx": (_I, [_P, _S, _P, _S, _P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                                  _P, _P, _P, _F, _P, _I, _I, _P, _P, _P]),
+    "spec_norm_rope_kv_mx_paged": (_I, [_P, _S, _P, _S, _P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P,
+                                        _I, _P, _P, _P, _P, _P, _F, _P, _I, _I, _P, _P, _P]),
+    "spec_unpack_kv_mx": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "spec_unpack_kv_mx_paged": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "spec_prompt_attention_mx": (_I, [_P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _P,
+                                      _P]),
+    "spec_prompt_attention_mx_paged": (_I, [_P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _F,
+                                            _P, _P, _P, _P]),
+    "spec_tree_attention_mx_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "spec_tree_attention_mx": (_I, [_P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _P, _P,
+                                    _SZ, _P]),
+    "spec_tree_attention_mx_paged": (_I, [_P, _S, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _F,
+                                          _P, _P, _P, _P, _SZ, _P]),
+    "spec_compact_tree_paged": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
 }
 
 _lib = None

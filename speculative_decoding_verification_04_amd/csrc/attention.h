@@ -20,7 +20,7 @@
 
 #include <type_traits>
 
-#include "cache_view.h"
+#include "mx.h"
 
 namespace specv {
 namespace attn {
@@ -147,6 +147,34 @@ struct Done {
   bool mine;
 };
 
+  // Takes infinities and NaNs out of the lane's own chunks of a V tile; whether
+  // there were any.  An exponent of all ones carries into the bit above it.
+  template <typename T, int DP, int RW>
+__device__ inline bool clean_share(char *buf) {
+  using S = Shape<T, DP, RW>;
+    u32x4 *own = reinterpret_cast<u32x4 *>(buf + S::kTile) + threadIdx.x;
+    constexpr uint32_t kExp = S::kElt == 2 ? 0x7f807f80u : 0x7f800000u, kOne = S::kElt == 2 ? 0x00800080u : 0x00800000u;
+    constexpr uint32_t kTop = S::kElt == 2 ? 0x80008000u : 0x80000000u;
+    uint32_t seen = 0;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const u32x4 x = own[i * kThreads];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) seen |= (x[j] & kExp) + kOne;
+    }
+    if (!(seen & kTop)) return false;
+    for (int i = 0; i < S::kLoads; ++i) {
+      u32x4 x = own[i * kThreads];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t odd = ((x[j] & kExp) + kOne) & kTop;   // the top bit of each value to clear
+        x[j] &= S::kElt == 2 ? ~((odd >> 15) * 0xffffu) : odd ? 0u : ~0u;
+      }
+      own[i * kThreads] = x;
+    }
+    return true;
+  }
+
 // Brings K and V tiles from the cache straight into LDS.  A wave's load writes
 // 64 consecutive 16-byte places, so a lane takes the chunk whose place its own
 // is.  Where a tile's rows all exist and the kRows rows of a load lie in one
@@ -231,31 +259,110 @@ struct Loader {
       if (has(i)) bring(P.c.k + off, P.c.v + off, i, buf);
     }
   }
-  // Takes infinities and NaNs out of the lane's own chunks of a V tile; whether
-  // there were any.  An exponent of all ones carries into the bit above it.
-  __device__ bool clean(char *buf) const {
-    u32x4 *own = reinterpret_cast<u32x4 *>(buf + S::kTile) + threadIdx.x;
-    constexpr uint32_t kExp = S::kElt == 2 ? 0x7f807f80u : 0x7f800000u, kOne = S::kElt == 2 ? 0x00800080u : 0x00800000u;
-    constexpr uint32_t kTop = S::kElt == 2 ? 0x80008000u : 0x80000000u;
-    uint32_t seen = 0;
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const u32x4 x = own[i * kThreads];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) seen |= (x[j] & kExp) + kOne;
-    }
-    if (!(seen & kTop)) return false;
-    for (int i = 0; i < S::kLoads; ++i) {
-      u32x4 x = own[i * kThreads];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t odd = ((x[j] & kExp) + kOne) & kTop;   // the top bit of each value to clear
-        x[j] &= S::kElt == 2 ? ~((odd >> 15) * 0xffffu) : odd ? 0u : ~0u;
-      }
-      own[i * kThreads] = x;
-    }
-    return true;
+  __device__ bool clean(char *buf) const { return clean_share<T, DP, RW>(buf); }
+};
+
+// Brings tiles of a cache of 4-bit numbers: codes and scales to registers one
+// tile before they are used, then as values of T to the places that Loader fills.
+// A lane takes kBytes of a row's codes at once, all of one scale.  Sixteen rows go
+// to the lanes in an order in which four neighbours have different turn()s in their
+// low bits, so that their writes meet no bank twice.
+template <typename T, int DP, int RW, bool PAGED>
+struct LoaderMx {
+  using S = Shape<T, DP, RW>;
+  static constexpr int kEach = S::kKT * DP / 2 / kThreads; // bytes of K's (or V's) codes a lane brings
+  static constexpr int kBytes = kEach < 16 ? kEach : 16;   // at once
+  static constexpr int kLoads = kEach / kBytes, kWords = kBytes / 4;
+  static constexpr int kPer = DP / 2 / kBytes;             // of those in a row
+  static_assert(kBytes >= 4 && kLoads * kBytes == kEach && kThreads % (16 * kPer) == 0, "whole rows for all lanes");
+  struct Raw {
+    uint32_t k[kWords], v[kWords];
+    int ks, vs;
+  };
+  const Params &P;
+  const Job &J;
+  int lrow, unit;                                         // the lane's row in the first load, and its share of a row
+  Raw raw[kLoads];                                        // of the tile fetched last
+  int page[kLoads];                                       // of the tile to be fetched next
+  bool bad;
+
+  __device__ LoaderMx(const Params &p, const Job &j) : P(p), J(j), bad(false) {
+    const int x = threadIdx.x / kPer;
+    lrow = (x & ~15) | ((x & 3) << 2) | ((x >> 2) & 3);
+    unit = threadIdx.x % kPer;
   }
+  __device__ int row(int i) const { return lrow + i * (kThreads / kPer); }
+  __device__ bool has() const { return DP == P.c.D || unit * 2 * kBytes < P.c.D; }
+  __device__ void clear(char *buf) const {
+    if (P.c.D == DP) return;
+    for (int x = threadIdx.x; x < S::kLds / 16; x += kThreads) reinterpret_cast<u32x4 *>(buf)[x] = u32x4{0, 0, 0, 0};
+  }
+  __device__ void pages(int t) {
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = min(t * S::kKT + row(i), J.total - 1);
+        page[i] = P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, r)];
+      }
+    }
+  }
+  // Asks for tile t (its pages are known), and for the pages of the next.
+  __device__ void fetch(int t) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = min(t * S::kKT + row(i), J.total - 1);
+      int plane = J.b, col = J.start_col + r;
+      if constexpr (PAGED) {
+        const bool ok = page[i] >= 0 && page[i] < P.c.planes;
+        bad |= !ok;
+        plane = ok ? page[i] : 0;
+        col = r - cache_page(P.c, r) * P.c.cols;
+      }
+      const long long at = (static_cast<long long>(plane) * P.c.H + J.h) * P.c.cols + col;
+      if (has()) {
+        const long long codes = at * (P.c.D / 2) + unit * kBytes;
+        const long long scales = at * (P.c.D / kMxBlock) + unit * 2 * kBytes / kMxBlock;
+        __builtin_memcpy(raw[i].k, __builtin_assume_aligned(P.c.k + codes, kBytes), kBytes);
+        __builtin_memcpy(raw[i].v, __builtin_assume_aligned(P.c.v + codes, kBytes), kBytes);
+        raw[i].ks = static_cast<uint8_t>(P.c.ks[scales]);
+        raw[i].vs = static_cast<uint8_t>(P.c.vs[scales]);
+      }
+    }
+    pages(min(t + 1, J.t1 - 1));
+  }
+  __device__ void put_values(const uint32_t (&codes)[kWords], int byte, int r, char *tile) const {
+    const float scale = mx_scale(byte);
+    constexpr int kChunks = 8 / S::kVec;                  // 16-byte chunks of eight values
+    char *to = tile + r * DP * S::kElt;
+    const int c0 = unit * kWords * kChunks, x = turn<S::kChunks>(r);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      T y[8];
+      mx_widen<T>(codes[w], scale, y);
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        u32x4 z;
+        __builtin_memcpy(&z, y + j * S::kVec, 16);
+        *reinterpret_cast<u32x4 *>(to + (((c0 + w * kChunks + j) ^ x) << 4)) = z;
+      }
+    }
+    if (byte > kMxTop) {                                  // rare: NaNs over what was put there
+      constexpr uint32_t kNan = S::kElt == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+      for (int c = 0; c < kWords * kChunks; ++c)
+        *reinterpret_cast<u32x4 *>(to + (((c0 + c) ^ x) << 4)) = u32x4{kNan, kNan, kNan, kNan};
+    }
+  }
+  // The fetched tile's values, to a buffer.
+  __device__ void put(char *buf) const {
+    if (!has()) return;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      put_values(raw[i].k, raw[i].ks, row(i), buf);
+      put_values(raw[i].v, raw[i].vs, row(i), buf + S::kTile);
+    }
+  }
+  // As Loader's, over any share of a V tile: the tile is whole when it is called.
+  __device__ bool clean(char *buf) const { return clean_share<T, DP, RW>(buf); }
 };
 
 // Which of cache rows [k0, k0 + 32) a query row sees, as bits.
@@ -418,7 +525,7 @@ __device__ inline void step(Rows<T, DP> &W, const char *lds, int kb0, float sl,
 // are not seen, and 0 * inf is not 0.  Such a tile's infinities and NaNs are
 // zero in LDS (clean()); here they are added to the query rows that see them,
 // from the cache itself.  Rare: one row of the cache after the other.
-template <typename T, int DP, int RW, bool PAGED>
+template <typename T, int DP, int RW, bool PAGED, bool MX>
 __device__ inline void add_odd(const Params &P, const Job &J, Rows<T, DP> &W, int k0,
                                const uint32_t (&vis)[Shape<T, DP, RW>::kNB]) {
   using S = Shape<T, DP, RW>;
@@ -434,6 +541,16 @@ __device__ inline void add_odd(const Params &P, const Job &J, Rows<T, DP> &W, in
       plane = P.c.table[static_cast<long long>(J.b) * P.c.max_pages + cache_page(P.c, r)];
       if (plane < 0 || plane >= P.c.planes) plane = 0;
       col = r - cache_page(P.c, r) * P.c.cols;
+    }
+    if constexpr (MX) {                                   // an odd scale is 32 NaNs
+      const char *scales = P.c.vs + cache_offset(P.c, plane, J.h, col, 1) / kMxBlock;
+#pragma unroll
+      for (int db = 0; db < DP / 32; ++db) {
+        const int byte = 32 * db < P.c.D ? static_cast<uint8_t>(scales[db]) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) W.o[db][i] += see && byte > kMxTop ? NAN : 0.0f;
+      }
+      continue;
     }
     const T *v = reinterpret_cast<const T *>(P.c.v + cache_offset(P.c, plane, J.h, col, S::kElt));
 #pragma unroll
@@ -465,20 +582,26 @@ __device__ inline void put4(char *out, int d0, int D, const float (&x)[4]) {
 // outputs (of KW waves on the same rows the kw-th has the kw-th DP / KW
 // elements) and with the rows' maxima and sums over all of them; all return
 // whether a bad page was met.
-template <typename T, int DP, int RW, bool PAGED, bool PROMPT, bool ONCE>
+template <typename T, int DP, int RW, bool PAGED, bool PROMPT, bool ONCE, bool MX>
 __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP, RW>::kKW> &D, char *buf0,
                             char *buf1) {
   using S = Shape<T, DP, RW>;
   const int lane = fresh(threadIdx.x & (kWave - 1)), n = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rw = wave % RW, kw = wave / RW;
-  Loader<T, DP, RW, PAGED, ONCE> ld(P, J);
+  typename std::conditional<MX, LoaderMx<T, DP, RW, PAGED>, Loader<T, DP, RW, PAGED, ONCE>>::type ld(P, J);
   ld.clear(buf0);
   ld.clear(buf1);
   if (P.c.D != DP) __syncthreads();                       // the zeros are there
   if (J.t0 < J.t1) {
     ld.pages(J.t0);
-    ld.load(J.t0, buf0);
-    ld.pages(min(J.t0 + 1, J.t1 - 1));
+    if constexpr (MX) {
+      ld.fetch(J.t0);
+      ld.put(buf0);
+      if (J.t0 + 1 < J.t1) ld.fetch(J.t0 + 1);
+    } else {
+      ld.load(J.t0, buf0);
+      ld.pages(min(J.t0 + 1, J.t1 - 1));
+    }
   }
   const int R = J.tokens * P.G;
   const int row = min(J.row0 + rw * 32 + n, R - 1);       // rows past the end repeat the last
@@ -510,12 +633,21 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
   const int mid = min(J.t1, plain / S::kKT);              // tiles before it every row sees whole
   __shared__ int flags[2];                                // V rows with infinities or NaNs; bad pages: once met, kept
   if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+  // 4-bit numbers: tile t + 1 waits in registers, and tile t + 2 is asked for.
   auto begin = [&](int t, char *next) __attribute__((always_inline)) {
+    if constexpr (MX) {
+      __syncthreads();                                    // tile t is in LDS, and tile t - 1 is read
+      if (t + 1 < J.t1) ld.put(next);
+      if (t + 2 < J.t1) ld.fetch(t + 2);
+      return;
+    }
     __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): this wave's part of tile t is in LDS
     __syncthreads();                                      // everyone's is, and tile t - 1 is read
     if (t + 1 < J.t1) {
-      ld.load(t + 1, next);
-      ld.pages(min(t + 2, J.t1 - 1));
+      if constexpr (!MX) {
+        ld.load(t + 1, next);
+        ld.pages(min(t + 2, J.t1 - 1));
+      }
     }
   };
   auto masked = [&](int t, char *now, char *next) __attribute__((always_inline)) {
@@ -532,7 +664,7 @@ __device__ inline bool walk(const Params &P, const Job &J, Done<DP, Shape<T, DP,
       odd = flags[0] != 0;
     }
     step<T, DP, RW, true>(W, now, kb0, P.sl, vis);
-    if (odd) add_odd<T, DP, RW, PAGED>(P, J, W, t * S::kKT + kb0, vis);
+    if (odd) add_odd<T, DP, RW, PAGED, MX>(P, J, W, t * S::kKT + kb0, vis);
   };
   int t = J.t0;
   if constexpr (RW == 4) {
@@ -661,12 +793,29 @@ __device__ inline void put_zeros(const Params &P, const Job &J, int rows) {
   }
 }
 
+// A cache as a call is given it: elements of dt, or the codes and scales of 4-bit
+// numbers.
+struct Given {
+  const void *data, *scales;
+  bool mx;
+};
+
+inline size_t given_bytes(const Given &kv, spec_dtype dt, int L, int planes, int H, int cols, int D) {
+  return kv.mx ? mx_rows(L, planes, H, cols) * (D / 2) : cache_bytes(dt, L, planes, H, cols, D);
+}
+inline size_t given_scales(const Given &kv, int L, int planes, int H, int cols, int D) {
+  return kv.mx ? mx_rows(L, planes, H, cols) * (D / kMxBlock) : 0;
+}
+
 // Host checks that both calls share; fills what they share.
-inline int fill(Params &P, const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int planes, int B,
+inline int fill(Params &P, const void *q, int64_t q_stride, const Given &kv, spec_dtype dt, int L, int planes, int B,
                 int H, int cols, int D, int layer, int G, const int32_t *table, int max_pages, bool paged,
                 const int32_t *end_col, const int32_t *kv_len, float scale, void *out, float *lse, int32_t *status) {
-  if (!q || !out) return SPEC_EINVAL;
-  const int err = cache_view(P.c, kv, dt, L, planes, H, cols, D, layer, table, max_pages, paged, end_col, kv_len);
+  if (!q || !out || (dt != SPEC_F32 && dt != SPEC_BF16)) return SPEC_EINVAL;
+  const int err = kv.mx ? mx_view(P.c, kv.data, kv.scales, L, planes, H, cols, D, layer, table, max_pages, paged,
+                                  end_col, kv_len)
+                        : cache_view(P.c, kv.data, dt, L, planes, H, cols, D, layer, table, max_pages, paged, end_col,
+                                     kv_len);
   if (err) return err;
   if (B < 1 || G < 1 || (!paged && planes != B)) return SPEC_EINVAL;
   if (!(scale > 0.0f) || scale > 2e38f) return SPEC_EINVAL;   // sl stays finite
@@ -674,7 +823,7 @@ inline int fill(Params &P, const void *q, int64_t q_stride, const void *kv, spec
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return SPEC_EINVAL;
   const int elt = dt == SPEC_BF16 ? 2 : 4;
   if (D * elt % 16 || q_stride < static_cast<long long>(H) * G * D || q_stride * elt % 16) return SPEC_EINVAL;
-  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4))
+  if (!aligned(q, 16) || !aligned(kv.data, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4))
     return SPEC_EINVAL;
   P.q = static_cast<const char *>(q);
   P.q_stride = q_stride * elt;

@@ -4,7 +4,9 @@
 // One layer of a cache is two arrays (K and V) of planes [planes][H][cols][D].
 // In the left-padded rectangle a plane is a sequence and row r of sequence b
 // lies at column E - n + r of plane b; in a page pool a plane is a page and
-// row r lies at column r % cols of plane table[b][r / cols].
+// row r lies at column r % cols of plane table[b][r / cols].  In a cache of 4-bit
+// numbers K and V are codes, [planes][H][cols][D / 2] bytes, and beside them lie
+// the scales of each 32 elements, [planes][H][cols][D / 32] bytes.
 #pragma once
 
 #include "common.h"
@@ -13,6 +15,7 @@ namespace specv {
 
 struct CacheView {
   char *k, *v;              // the layer's K and V planes
+  char *ks, *vs;            // 4-bit numbers: their scales; else NULL
   int H, cols, D, planes;   // cols: C of the rectangle, or the page size
   const int32_t *table;     // block table [B][max_pages], or NULL: a rectangle
   int max_pages;
@@ -52,19 +55,14 @@ __host__ __device__ inline long long cache_capacity(const CacheView &c) {
 
 // Host checks shared by the calls that take a cache; fills the view of one
 // layer.  Returns SPEC_OK or SPEC_EINVAL.
-inline int cache_view(CacheView &c, const void *kv, spec_dtype dt, int L, int planes, int H, int cols, int D,
-                      int layer, const int32_t *table, int max_pages, bool paged, const int32_t *end_col,
-                      const int32_t *kv_len) {
-  if (!kv || !kv_len || (paged ? !table : !end_col)) return SPEC_EINVAL;
-  if (dt != SPEC_F32 && dt != SPEC_BF16) return SPEC_EINVAL;
+inline int cache_shape(CacheView &c, int L, int planes, int H, int cols, int D, int layer, const int32_t *table,
+                       int max_pages, bool paged, const int32_t *end_col, const int32_t *kv_len) {
+  if (!kv_len || (paged ? !table : !end_col)) return SPEC_EINVAL;
   if (L < 1 || planes < 1 || H < 1 || cols < 1 || D < 1 || layer < 0 || layer >= L) return SPEC_EINVAL;
   // row numbers, rounded up to whole tiles, stay below 2^31
   if (paged && max_pages < 1) return SPEC_EINVAL;
   if ((paged ? static_cast<long long>(max_pages) : 1ll) * cols > INT32_MAX - 512) return SPEC_EINVAL;
-  const long long elt = dt == SPEC_BF16 ? 2 : 4;
-  const long long half = static_cast<long long>(planes) * H * cols * D * elt;  // one layer's K
-  c.k = static_cast<char *>(const_cast<void *>(kv)) + 2 * half * layer;
-  c.v = c.k + half;
+  c.ks = c.vs = nullptr;
   c.H = H;
   c.cols = cols;
   c.D = D;
@@ -74,6 +72,19 @@ inline int cache_view(CacheView &c, const void *kv, spec_dtype dt, int L, int pl
   c.end_col = paged ? nullptr : end_col;
   c.kv_len = kv_len;
   cache_divisor(c);
+  return SPEC_OK;
+}
+
+inline int cache_view(CacheView &c, const void *kv, spec_dtype dt, int L, int planes, int H, int cols, int D,
+                      int layer, const int32_t *table, int max_pages, bool paged, const int32_t *end_col,
+                      const int32_t *kv_len) {
+  if (!kv || (dt != SPEC_F32 && dt != SPEC_BF16)) return SPEC_EINVAL;
+  const int err = cache_shape(c, L, planes, H, cols, D, layer, table, max_pages, paged, end_col, kv_len);
+  if (err) return err;
+  const long long elt = dt == SPEC_BF16 ? 2 : 4;
+  const long long half = static_cast<long long>(planes) * H * cols * D * elt;  // one layer's K
+  c.k = static_cast<char *>(const_cast<void *>(kv)) + 2 * half * layer;
+  c.v = c.k + half;
   return SPEC_OK;
 }
 

@@ -81,24 +81,6 @@ typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 // slots the forward wrote.
 __device__ inline int kept_slots(const RealignParams &P, int b) { return min(P.emit_count[b], P.slots); }
 
-template <int VB>
-struct VecOf;
-template <>
-struct VecOf<16> { using T = uint4; };
-template <>
-struct VecOf<8> { using T = uint2; };
-template <>
-struct VecOf<4> { using T = uint32_t; };
-template <>
-struct VecOf<2> { using T = uint16_t; };
-
-// Makes the compiler hold a loaded value in registers at this point, so the
-// load has completed (s_waitcnt) before whatever follows.
-__device__ inline void hold(uint4 v) { asm volatile("" ::"v"(v.x), "v"(v.y), "v"(v.z), "v"(v.w)); }
-__device__ inline void hold(uint2 v) { asm volatile("" ::"v"(v.x), "v"(v.y)); }
-__device__ inline void hold(uint32_t v) { asm volatile("" ::"v"(v)); }
-__device__ inline void hold(uint16_t v) { asm volatile("" ::"v"(static_cast<uint32_t>(v))); }
-
 // Streaming (non-temporal) access: every moved byte is read once and written once.
 template <typename VT>
 __device__ inline VT stream_ld(const VT *p) { return __builtin_nontemporal_load(p); }

@@ -27,6 +27,25 @@ inline int launch_status() {
 }
 
 // -------------------------------------------------------------- device ----
+// An unsigned vector of VB bytes.
+template <int VB>
+struct VecOf;
+template <>
+struct VecOf<16> { using T = uint4; };
+template <>
+struct VecOf<8> { using T = uint2; };
+template <>
+struct VecOf<4> { using T = uint32_t; };
+template <>
+struct VecOf<2> { using T = uint16_t; };
+
+// Makes the compiler hold a loaded value in registers at this point, so the
+// load has completed (s_waitcnt) before whatever follows.
+__device__ inline void hold(uint4 v) { asm volatile("" ::"v"(v.x), "v"(v.y), "v"(v.z), "v"(v.w)); }
+__device__ inline void hold(uint2 v) { asm volatile("" ::"v"(v.x), "v"(v.y)); }
+__device__ inline void hold(uint32_t v) { asm volatile("" ::"v"(v)); }
+__device__ inline void hold(uint16_t v) { asm volatile("" ::"v"(static_cast<uint32_t>(v))); }
+
 // Relaxed agent-scope (whole-GPU) atomic load: reads through the per-XCD L2s.
 template <typename T>
 __device__ inline T load_agent(const T *p) {

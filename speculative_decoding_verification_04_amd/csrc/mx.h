@@ -72,35 +72,44 @@ __device__ inline int mx_scale_byte(uint32_t top) {
   return min(max(static_cast<int>((top + 0x200000u) >> 23) - 2, 2), kMxTop);
 }
 
-// Codes of N (4 or 8) elements, for a scale byte of mx_scale_byte().
+// Codes of N (4 or 8) elements, for a scale byte of mx_scale_byte().  The instruction
+// rounds to the nearest code, ties to the even one, and gives 6 for more.
 template <int N>
 __device__ inline uint32_t mx_codes(const float (&x)[N], int byte) {
   if (byte == kMxNan) return 0u;
-  const float scale = mx_scale(byte), most = 6.0f * scale;
-  float y[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) y[j] = fminf(fmaxf(x[j], -most), most);
-  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], scale, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], scale, 1);
+  const float scale = mx_scale(byte);
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0], x[1], scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], scale, 1);
   if constexpr (N == 8) {
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], scale, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], scale, 3);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], scale, 3);
   }
   return c;
 }
 
-// A double as the float on its way to a code: rounded so that no border between
-// codes or scales is reached or passed that the double itself does not reach or
-// pass.  Borders are floats with few bits, so their last bit is 0: where the
-// nearest float is not the double itself and its last bit is 0, the neighbour on
-// the double's side is taken.
+// The same of eight elements of bf16, in pairs.
+__device__ inline uint32_t mx_codes_bf16(const uint32_t (&x)[4], int byte) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  if (byte == kMxNan) return 0u;
+  const float scale = mx_scale(byte);
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0u, __builtin_bit_cast(bf16x2, x[0]), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[1]), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[2]), scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[3]), scale, 3);
+}
+
+// A double as the float on its way to a code: cut to 20 bits of its fraction, with the
+// last of them set where anything was cut off, so that it is on the double's side of
+// every border (borders have few bits).  Past float32's range: infinity; between half
+// and all of the smallest normal number, three quarters of it, and 0 below.
 __device__ inline float mx_sided(double x) {
-  const float f = static_cast<float>(x);
-  const double off = x - static_cast<double>(f);
-  const uint32_t u = __float_as_uint(f);
-  if (off == 0.0 || (u & 1u) || (u & 0x7fffffffu) >= 0x7f800000u) return f;
-  if ((u & 0x7fffffffu) == 0u) return __uint_as_float((x < 0.0 ? 0x80000000u : 0u) | 1u);   // below the smallest float
-  return __uint_as_float((off > 0.0) == (f > 0.0f) ? u + 1u : u - 1u);
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t high = static_cast<uint32_t>(u >> 32), size = (high & 0x7fffffffu) | (static_cast<uint32_t>(u) ? 1u : 0u);
+  const uint32_t base = 896u << 20;                       // what exponents differ by
+  uint32_t bits = (size - base) << 3;
+  if (size < base + (1u << 20)) bits = size > base ? 0x00600000u : 0u;
+  if (size >= base + (255u << 20)) bits = size > 0x7ff00000u ? 0x7fc00000u : 0x7f800000u;
+  return __uint_as_float(bits | (high & 0x80000000u));
 }
 
 }  // namespace specv

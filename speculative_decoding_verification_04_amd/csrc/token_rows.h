@@ -74,5 +74,66 @@ __device__ inline void write_status(const TokenRows &P, int b) {
   if (lane == 0) P.status[b] = st;
 }
 
+// Where a token's rows lie; a wave finds it.
+constexpr long long kNotHeld = -1, kNoSequence = -2;
+struct Place {
+  int row;               // in its sequence
+  long long at;          // of head 0 in the layer's K or V, as (plane, head, column) counts; kNotHeld: not to
+};                       // be touched (a status, a bad page); kNoSequence
+
+// What finding it reads first, so that a kernel can ask for it ahead of its data
+// (loads come back in order): the end column, and the first 64 sequences' state.  What
+// is absent is read from where something is, since a branch would end in a wait.
+struct Early {
+  int E, lo, hi, n;
+};
+__device__ inline Early early_of(const TokenRows &P, int t) {
+  const int32_t *any = P.c.kv_len;
+  const int i = min(static_cast<int>(threadIdx.x & (kWave - 1)), P.B - 1);
+  Early e;
+  e.E = *(P.c.table ? any : P.c.end_col);
+  e.lo = *(P.cu ? P.cu + i : any);
+  e.hi = *(P.cu ? P.cu + i + 1 : any);
+  e.n = P.c.kv_len[P.cu ? i : t / max(P.N, 1)];
+  return e;
+}
+
+__device__ inline Place place_of(const TokenRows &P, int t, const Early &early) {
+  const int lane = threadIdx.x & (kWave - 1), E = P.c.table ? 0 : early.E;
+  int b = -1, t0 = 0, t1 = 0, n = early.n;
+  if (P.cu) {
+    // the first sequence that holds token t, with no fall before it
+    for (int b0 = 0; b0 < P.B; b0 += kWave) {
+      const bool is = b0 + lane < P.B;
+      const int i = min(b0 + lane, P.B - 1), lo = b0 ? P.cu[i] : early.lo, hi = b0 ? P.cu[i + 1] : early.hi;
+      const uint64_t who = __ballot(is && lo <= t && t < hi), falls = __ballot(is && lo > hi);
+      if (who | falls) {
+        const int l = __ffsll(static_cast<unsigned long long>(who | falls)) - 1;
+        if (who >> l & 1) {
+          b = b0 + l;
+          t0 = read_lane(lo, l);
+          t1 = read_lane(hi, l);
+          n = b0 ? P.c.kv_len[b] : read_lane(early.n, l);
+        }
+        break;
+      }
+    }
+    if (b < 0) return Place{0, kNoSequence};
+  } else {
+    b = t / P.N;
+  }
+  const Span s = span_of(P, b, t0, t1, n, E);
+  const int row = s.row0 + (t - s.t0);
+  if (s.st) return Place{row, kNotHeld};
+  int plane = b, col = E - n + row;
+  if (P.c.table) {
+    const int i = cache_page(P.c, row);
+    plane = P.c.table[static_cast<long long>(b) * P.c.max_pages + i];
+    col = row - i * P.c.cols;
+    if (plane < 0 || plane >= P.c.planes) return Place{row, kNotHeld};
+  }
+  return Place{row, static_cast<long long>(plane) * P.c.H * P.c.cols + col};
+}
+
 }  // namespace
 }  // namespace specv

@@ -23,47 +23,9 @@ struct UnpackParams : TokenRows {
   int per, groups;           // tokens of a workgroup; workgroups that have tokens
 };
 
-// The row of token t in the layer's K or V, head 0; -1: zeros; -2: a token of no sequence.
-__device__ inline long long row_of(const UnpackParams &P, int t) {
-  const int lane = threadIdx.x & (kWave - 1), E = P.c.table ? 0 : *P.c.end_col;
-  int b = -1, t0 = 0, t1 = 0;
-  if (P.cu) {
-    // the first sequence that holds token t, with no fall before it
-    for (int b0 = 0; b0 < P.B; b0 += kWave) {
-      const bool is = b0 + lane < P.B;
-      const int i = min(b0 + lane, P.B - 1), lo = P.cu[i], hi = P.cu[i + 1];
-      const uint64_t who = __ballot(is && lo <= t && t < hi), falls = __ballot(is && lo > hi);
-      if (who | falls) {
-        const int l = __ffsll(static_cast<unsigned long long>(who | falls)) - 1;
-        if (who >> l & 1) {
-          b = b0 + l;
-          t0 = read_lane(lo, l);
-          t1 = read_lane(hi, l);
-        }
-        break;
-      }
-    }
-    if (b < 0) return -2;
-  } else {
-    b = t / P.N;
-  }
-  const int n = P.c.kv_len[b];
-  const Span s = span_of(P, b, t0, t1, n, E);
-  if (s.st) return -1;
-  const int row = s.row0 + (t - s.t0);
-  int plane = b, col = E - n + row;
-  if (P.c.table) {
-    const int i = cache_page(P.c, row);
-    plane = P.c.table[static_cast<long long>(b) * P.c.max_pages + i];
-    col = row - i * P.c.cols;
-    if (plane < 0 || plane >= P.c.planes) return -1;
-  }
-  return static_cast<long long>(plane) * P.c.H * P.c.cols + col;
-}
-
 template <typename T>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(UnpackParams P) {
-  __shared__ long long at[kMaxTokens];
+  __shared__ long long at[kMaxTokens];                   // each token's Place::at
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (blockIdx.x >= static_cast<unsigned>(P.groups)) {
     write_status(P, (blockIdx.x - P.groups) * kWaves + wave);
@@ -71,8 +33,8 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(UnpackParams P) {
   }
   const int first = blockIdx.x * P.per, count = min(P.per, P.T - first);
   for (int i = wave; i < count; i += kWaves) {
-    const long long r = row_of(P, first + i);
-    if ((threadIdx.x & (kWave - 1)) == 0) at[i] = r;
+    const Place p = place_of(P, first + i, early_of(P, first + i));
+    if ((threadIdx.x & (kWave - 1)) == 0) at[i] = p.at;
   }
   __syncthreads();
   const int D = P.c.D, row_items = D / 8, half = P.c.H * row_items, items = 2 * half;   // of a token
@@ -91,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(UnpackParams P) {
       const bool is_v = y >= half;
       const int z = is_v ? y - half : y, h = z / row_items, d = (z - h * row_items) * 8;
       const long long r0 = at[i];
-      if (r0 == -2) continue;
+      if (r0 == kNoSequence) continue;
       to[u] = (is_v ? P.v_out : P.k_out) + (static_cast<long long>(first + i) * half * 8 + z * 8) * sizeof(T);
       if (r0 < 0) continue;
       const long long row = r0 + static_cast<long long>(h) * P.c.cols;

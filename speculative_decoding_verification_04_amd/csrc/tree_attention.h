@@ -27,7 +27,7 @@
 // 4: 18 us; one token over 1100 rows: 12 us, the latency of two launches.
 #pragma once
 
-#include "attention.h"
+#include "few_rows.h"
 
 namespace specv {
 namespace {
@@ -38,19 +38,29 @@ inline int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Workgroups that join `rows` query rows: a wave each.
 inline long long join_grid(long long rows) { return (rows + kThreads / kWave - 1) / (kThreads / kWave); }
 
-// How a call is cut: waves side by side, row tiles, pieces aimed at.
+constexpr int kWholeRows = 1024;
+
+// How a call is cut: waves side by side, row tiles, pieces aimed at; few: by few_kernel.
 struct Plan {
-  int rw, kt, row_tiles, target;
+  bool few;
+  int rw, kt, row_tiles, target, threads;
   long long groups, tiles, slots;   // tiles, slots (pieces): the most that the cache can give
 };
 
-inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_dtype dt) {
+inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_dtype dt, bool mx) {
   Plan p;
   const long long R = static_cast<long long>(N) * G;
   // two buffers of 128 / rw cache rows (K and V, padded to dp) have to fit LDS
   const int row = dp_of(D) * (dt == SPEC_BF16 ? 2 : 4), least = row <= 256 ? 1 : row <= 512 ? 2 : 4;
   p.rw = R > 64 || least == 4 ? 4 : R > 32 || least == 2 ? 2 : 1;
   p.kt = p.rw == 4 ? (dt == SPEC_BF16 ? 64 : 32) : 128 / p.rw;
+  p.few = mx && R <= 64;
+  if (p.few) {
+    p.rw = R > 32 ? 2 : 1;
+    p.kt = 32;
+  }
+  const bool pairs = p.few && p.rw == 2 && dt == SPEC_BF16 && D <= 128;        // two blocks of query rows in a wave
+  p.threads = p.few && D <= 128 && !pairs ? 2 * kThreads : kThreads;
   p.row_tiles = static_cast<int>((R + 32 * p.rw - 1) / (32 * p.rw));
   p.groups = static_cast<long long>(B) * H * p.row_tiles;
   p.tiles = p.groups * ((max_rows + p.kt - 1) / p.kt);
@@ -58,15 +68,23 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   // a row takes up to 256 bytes and a workgroup more than 32 query rows.  (512 for
   // all: 66-node float32 trees, 28 heads of 128, took 46 us instead of 37.)  The
   // kernels of bf16 heads up to 64 would fit once more on a CU than this counts.
-  p.target = p.rw > 1 && row <= 256 ? 512 : 256;
+  p.target = (p.few ? pairs : p.rw > 1 && row <= 256) ? 512 : 256;
   p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
+  if (p.few) {
+    // Not cut at all, and so not joined: where the groups alone fill the chip, or where
+    // a group's longest walk takes no longer than the second launch.
+    if (p.groups >= p.target || max_rows <= kWholeRows) p.target = 0;
+    // the kernel's second look keeps up to 64 sequences' pieces to the target
+    if (p.target == 0) p.slots = p.groups;
+    else if (B <= kWave) p.slots = p.target;
+  }
   if (p.slots > p.tiles) p.slots = p.tiles;
   return p;
 }
 
 // Both launches fit, and the kernel's sums of tiles (with a target added) stay below 2^31.
 inline bool plan_fits(const Plan &p, long long rows) {
-  return p.tiles <= INT32_MAX - p.target && launchable(p.slots, kThreads) && launchable(join_grid(rows), kThreads);
+  return p.tiles <= INT32_MAX - p.target && launchable(p.slots, p.threads) && launchable(join_grid(rows), kThreads);
 }
 
 // Workspace: a slot for each piece, and each group's pieces.
@@ -103,27 +121,28 @@ __device__ inline int tree_tiles(const Params &P, int n, int E, int kt) {
   return tree_status(P, n, E) ? 0 : static_cast<int>((static_cast<long long>(n) + P.N + kt - 1) / kt);
 }
 
-template <typename T, int DP, int RW, bool PAGED, bool ONCE, bool MX>
-__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2 : 1) void tree_kernel(Params P) {
-  using S = Shape<T, DP, RW>;
-  __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
-  __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), rw = wave % RW;
+// What a workgroup does: finds its piece, walks it by `walk` and stores the results.
+// KT: rows of a tile that pieces are counted in; KW: waves behind each other.
+template <typename T, int DP, int RW, bool PAGED, int KT, int KW, class Walk>
+__device__ inline void tree_piece(const Params &P, Walk walk) {
+  const int lane = threadIdx.x & (kWave - 1);
   const int H = P.c.H, each = H * P.row_tiles, E = PAGED ? 0 : *P.c.end_col;
   // all tiles of the call; the first 64 sequences' stay in the lanes
   const int n0 = lane < P.B ? P.c.kv_len[lane] : -1;
-  const int tiles0 = tree_tiles(P, n0, E, S::kKT);
+  const int tiles0 = tree_tiles(P, n0, E, KT);
   int total = tiles0;                                     // the host has seen that it fits
-  for (int b = lane + kWave; b < P.B; b += kWave) total += tree_tiles(P, P.c.kv_len[b], E, S::kKT);
+  for (int b = lane + kWave; b < P.B; b += kWave) total += tree_tiles(P, P.c.kv_len[b], E, KT);
   total = wave_reduce(total, [](int a, int c) { return a + c; }) * each;
   // Tiles of a piece, at most: so many that the pieces fit the chip at once.  A
   // few workgroups more than that would run alone behind all the others: 16-node
   // trees over 32 sequences of 512 .. 4096 rows took 74 us so and 84 us without
   // the second look, 255-node trees over 32k rows 324 and 410 us.  It is not taken
   // for more than 64 sequences, nor where the groups alone exceed the target.
-  int per = max(1, (total + P.target - 1) / P.target);
+  const bool whole = P.target == 0;                       // no group is cut
+  int per = whole ? INT32_MAX : max(1, (total + P.target - 1) / P.target);
+  auto pieces_of = [&](int tiles) { return whole ? min(tiles, 1) : (tiles + per - 1) / per; };
   if (P.B <= kWave && each * P.B <= P.target)
-    while (per > 1 && wave_reduce((tiles0 + per - 1) / per, [](int a, int c) { return a + c; }) * each > P.target)
+    while (per > 1 && wave_reduce(pieces_of(tiles0), [](int a, int c) { return a + c; }) * each > P.target)
       per += (per + 15) / 16;
   // this workgroup's sequence: the pieces are numbered in the order of sequence, head, row tile
   Job J;
@@ -132,7 +151,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
   for (int b0 = 0; b0 < P.B; b0 += kWave) {
     const int b = b0 + lane;
     const int nb = b0 == 0 ? n0 : b < P.B ? P.c.kv_len[b] : -1;
-    const int tb = b0 == 0 ? tiles0 : tree_tiles(P, nb, E, S::kKT), pb = (tb + per - 1) / per;
+    const int tb = b0 == 0 ? tiles0 : tree_tiles(P, nb, E, KT), pb = pieces_of(tb);
     const int upto = wave_incl_scan(pb * each);
     const uint64_t who = __ballot(first + upto > static_cast<int>(blockIdx.x));
     if (who) {
@@ -158,30 +177,33 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
     const int size = tiles / pieces, more = tiles - size * pieces;   // the first `more` pieces are one tile longer
     J.t0 = i * size + min(i, more);
     J.t1 = J.t0 + size + (i < more ? 1 : 0);
-    Done<DP, S::kKW> D;
-    const bool bad = walk<T, DP, RW, PAGED, false, ONCE, MX>(P, J, D, buf0, buf1);
-    if (pieces == 1) {
-      put_rows<T>(P, J, D, sees_any(P, J.b, D.token));
-      if (P.status && J.h == 0 && J.row0 == 0 && threadIdx.x == 0) P.status[J.b] = bad ? SPEC_ST_BAD_STATE : 0;
-    } else {
-      if (D.mine) {
+    // results of 32 query rows, the rw-th of the tile; sees: whether they see anything
+    auto store = [&](const Done<DP, KW> &D, int rw, bool sees) __attribute__((always_inline)) {
+      if (pieces == 1) {
+        put_rows<T>(P, J, D, sees);
+      } else if (D.mine) {
         const long long row = static_cast<long long>(blockIdx.x) * (32 * RW) + rw * 32 + (lane & 31);
         char *o = reinterpret_cast<char *>(P.part_o + row * P.c.D);
 #pragma unroll
-        for (int q = 0; q < DP / 8 / S::kKW; ++q) {
+        for (int q = 0; q < DP / 8 / KW; ++q) {
           const float x[4] = {D.o[q][0], D.o[q][1], D.o[q][2], D.o[q][3]};
-          put4<float>(o, 8 * (D.kw * (DP / 8 / S::kKW) + q) + 4 * (lane >> 5), P.c.D, x);
+          put4<float>(o, 8 * (D.kw * (DP / 8 / KW) + q) + 4 * (lane >> 5), P.c.D, x);
         }
         if (lane < 32 && D.kw == 0) P.part_ml[row] = make_float2(D.m, D.l);
       }
-      if (threadIdx.x == 0) P.part_bad[blockIdx.x] = bad;
+    };
+    const bool bad = walk(J, store);
+    if (pieces == 1) {
+      if (P.status && J.h == 0 && J.row0 == 0 && threadIdx.x == 0) P.status[J.b] = bad ? SPEC_ST_BAD_STATE : 0;
+    } else if (threadIdx.x == 0) {
+      P.part_bad[blockIdx.x] = bad;
     }
     if (i == 0 && threadIdx.x == 0)
       reinterpret_cast<int2 *>(P.pieces)[static_cast<long long>(J.b) * each + g] = make_int2(blockIdx.x, pieces);
   }
   // sequences that are not read: zeros
   for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-    const int st = tree_status(P, P.c.kv_len[b], E);
+    const int st = tree_status(P, b < kWave ? read_lane(n0, b) : P.c.kv_len[b], E);
     if (!st) continue;
     J.token0 = static_cast<long long>(b) * P.N;
     J.row0 = 0;
@@ -190,6 +212,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
     for (int x = threadIdx.x; x < each; x += kThreads)
       reinterpret_cast<int2 *>(P.pieces)[static_cast<long long>(b) * each + x] = make_int2(0, 0);
   }
+}
+
+template <typename T, int DP, int RW, bool PAGED, bool ONCE, bool MX>
+__global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2 : 1) void tree_kernel(Params P) {
+  using S = Shape<T, DP, RW>;
+  __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
+  __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
+  tree_piece<T, DP, RW, PAGED, S::kKT, S::kKW>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
+    Done<DP, S::kKW> D;
+    const bool bad = walk<T, DP, RW, PAGED, false, ONCE, MX>(P, J, D, buf0, buf1);
+    store(D, __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % RW, sees_any(P, J.b, D.token));
+    return bad;
+  });
+}
+
+// Few query rows over 4-bit numbers: RW waves side by side, or QB blocks of rows in each.
+template <typename T, int D, int RW, int QB, bool PAGED>
+__global__ __launch_bounds__((Few<T, D, RW, QB>::kThreads), D <= 128 ? 2 : 1) void few_kernel(Params P) {
+  using F = Few<T, D, RW, QB>;
+  __shared__ __attribute__((aligned(16))) char lds[F::kLds];
+  tree_piece<T, D, RW * QB, PAGED, 32, F::kKW>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
+    return few_walk<T, D, RW, QB, PAGED>(P, J, store, lds);
+  });
 }
 
 // Joins the pieces of the groups that were cut, one wave for each query row,
@@ -293,9 +338,35 @@ void launch_rows(const Params &P, unsigned grid, hipStream_t s) {
   launch_once<T, DP, RW, false, MX>(P, grid, s);
 }
 
+template <typename T, int D, int RW, int QB>
+void launch_few_rows(const Params &P, unsigned grid, hipStream_t s) {
+  constexpr int kLanes = Few<T, D, RW, QB>::kThreads;
+  if (P.c.table)
+    hipLaunchKernelGGL((few_kernel<T, D, RW, QB, true>), dim3(grid), dim3(kLanes), 0, s, P);
+  else
+    hipLaunchKernelGGL((few_kernel<T, D, RW, QB, false>), dim3(grid), dim3(kLanes), 0, s, P);
+}
+
+// More than 32 query rows: two blocks in a wave where its registers hold them, so that
+// a conversion serves 64 rows; else two waves.
+template <typename T, int D>
+void launch_few(const Params &P, const Plan &p, unsigned grid, hipStream_t s) {
+  if (p.rw == 1) return launch_few_rows<T, D, 1, 1>(P, grid, s);
+  if constexpr (sizeof(T) == 2 && D <= 128) launch_few_rows<T, D, 1, 2>(P, grid, s);
+  else launch_few_rows<T, D, 2, 1>(P, grid, s);
+}
+
 template <typename T, int DP, bool MX>
 void launch_tree(const Params &P, const Plan &p, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.slots);
+  if constexpr (MX) {
+    if (p.few) {
+      if constexpr (DP == 256) {
+        if (P.c.D == 192) return launch_few<T, 192>(P, p, grid, s);
+      }
+      return launch_few<T, DP>(P, p, grid, s);
+    }
+  }
   if (p.rw == 4) return launch_rows<T, DP, 4, MX>(P, grid, s);
   if constexpr (sizeof(T) * DP <= 512) {
     if (p.rw == 2) return launch_rows<T, DP, 2, MX>(P, grid, s);
@@ -309,6 +380,7 @@ int launch_both(const Params &P, const Plan &p, hipStream_t s) {
   launch_tree<T, DP, MX>(P, p, s);
   const int st = launch_status();
   if (st != SPEC_OK) return st;
+  if (p.target == 0) return SPEC_OK;
   const unsigned joins = static_cast<unsigned>(join_grid(static_cast<long long>(P.B) * P.c.H * P.N * P.G));
   hipLaunchKernelGGL((join_kernel<T, DP>), dim3(joins), dim3(kThreads), 0, s, P, 32 * p.rw);
   return launch_status();
@@ -334,7 +406,7 @@ int tree_call(const void *q, int64_t q_stride, const Given &kv, spec_dtype dt, i
   if (!aligned(mask, 4)) return SPEC_EINVAL;
   const long long tokens = static_cast<long long>(B) * N, rows = tokens * H * G;
   if (rows >= INT32_MAX) return SPEC_EINVAL;
-  const Plan p = plan_of(B, N, H, G, D, cache_capacity(P.c), dt);
+  const Plan p = plan_of(B, N, H, G, D, cache_capacity(P.c), dt, MX);
   if (!plan_fits(p, rows)) return SPEC_EINVAL;
   const size_t elt = dt == SPEC_BF16 ? 2 : 4, hd = static_cast<size_t>(H) * G * D, b4 = static_cast<size_t>(B) * 4;
   const int words = (N + 31) / 32;
@@ -367,13 +439,13 @@ int tree_call(const void *q, int64_t q_stride, const Given &kv, spec_dtype dt, i
   return dt == SPEC_BF16 ? launch_all<__bf16, MX>(P, p, s) : launch_all<float, MX>(P, p, s);
 }
 
-inline size_t tree_workspace_bytes(int B, int N, int H, int G, int D, int max_rows, spec_dtype dt) {
+inline size_t tree_workspace_bytes(int B, int N, int H, int G, int D, int max_rows, spec_dtype dt, bool mx) {
   if (B < 1 || N < 1 || N > SPEC_TREE_MAX_N || H < 1 || G < 1 || D < 1 || D > SPEC_ATTN_MAX_D || max_rows < 1) return 0;
   if (dt != SPEC_F32 && dt != SPEC_BF16) return 0;
   if (static_cast<long long>(H) * G >= INT32_MAX / SPEC_ATTN_MAX_D) return 0;
   const long long rows = static_cast<long long>(B) * N * H * G;
   if (rows >= INT32_MAX) return 0;
-  const Plan p = plan_of(B, N, H, G, D, max_rows, dt);
+  const Plan p = plan_of(B, N, H, G, D, max_rows, dt, mx);
   return plan_fits(p, rows) ? space_of(p, D).end : 0;
 }
 

@@ -5,7 +5,7 @@ using namespace specv;
 
 extern "C" size_t spec_tree_attention_workspace_bytes(int B, int N, int H, int G, int D, int max_rows,
                                                       spec_dtype dt) {
-  return tree_workspace_bytes(B, N, H, G, D, max_rows, dt);
+  return tree_workspace_bytes(B, N, H, G, D, max_rows, dt, false);
 }
 
 extern "C" int spec_tree_attention(const void *q, int64_t q_stride, const void *kv, spec_dtype dt, int L, int B, int H,

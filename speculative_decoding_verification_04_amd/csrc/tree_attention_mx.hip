@@ -5,7 +5,7 @@ using namespace specv;
 
 extern "C" size_t spec_tree_attention_mx_workspace_bytes(int B, int N, int H, int G, int D, int max_rows,
                                                          spec_dtype dt) {
-  return D % 64 ? 0 : tree_workspace_bytes(B, N, H, G, D, max_rows, dt);
+  return D % 64 ? 0 : tree_workspace_bytes(B, N, H, G, D, max_rows, dt, true);
 }
 
 extern "C" int spec_tree_attention_mx(const void *q, int64_t q_stride, const uint8_t *codes, const uint8_t *scales,

@@ -26,9 +26,7 @@ namespace attn {
 
 template <typename T, int D, int RW, int QB>
 struct Few {
-  // two waves a SIMD, in one workgroup or two (more query rows: pieces of half the size
-  // balance sequences of unequal lengths), or one where registers are short
-  static constexpr int kWaves = D <= 128 && QB == 1 ? 8 : 4;
+  static constexpr int kWaves = D <= 128 ? 8 : 4;         // two a SIMD, or one where registers are short
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kKW = kWaves / RW;                 // waves behind each other
   static constexpr int kParts = sizeof(T) == 2 ? 1 : 3;   // bf16 parts of a number
@@ -36,12 +34,11 @@ struct Few {
   static constexpr int kAhead = QB == 1 ? 2 : 1;          // blocks in registers before they are used
   static constexpr int kRow = (D <= 64 ? 64 : D <= 128 ? 128 : 256) * 2;   // bytes of a row of V in LDS
   static constexpr int kStage = 32 * kRow;                // V of one wave
-  static constexpr int kJoinD = QB == 1 ? D : 64;         // elements of the outputs joined at a time
-  static constexpr int kJoin = 32 * kJoinD * 4;           // those of 32 rows of one wave
+  static constexpr int kJoin = 32 * D * 4;                // outputs of 32 rows of one wave
   static constexpr int kEach = kStage > kJoin ? kStage : kJoin;
   static constexpr int kQueries = QB == 1 ? 0 : QB * 4 * kShares * kWave * 16;   // operands of all waves
   static constexpr int kLds = kWaves * kEach + kQueries;
-  static_assert((RW == 1 || QB == 1) && kJoinD % (D / kKW) == 0, "one or the other; a wave's share is joined at once");
+  static_assert(RW == 1 || QB == 1, "one or the other");
 };
 
 // A lane's part of a block of 32 cache rows: row lane % 32, blocks 2 i + lane / 32.
@@ -380,50 +377,44 @@ __device__ inline bool few_walk(const Params &P, const Job &J, Store store, char
     }
   }
 
-  // Join the waves behind each other, as walk() does: 32 rows of each, and kJoinD
-  // elements of the outputs, at a time.
+  // Join the waves behind each other, as walk() does, 32 rows of each at a time.
   __shared__ float2 jm[F::kWaves][32];
   __shared__ int flag;
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    Done<D, F::kKW> R;
     const float total = half_sum(l[b]);
+    __syncthreads();                                      // the stages, or the outputs before, are read
+    if (threadIdx.x == 0 && b == 0) flag = 0;
+    f32x4 *mine = reinterpret_cast<f32x4 *>(lds + wave * F::kEach) + hf * 32 + n;
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += F::kJoinD) {
-      __syncthreads();                                    // the stages, or the outputs before, are read
-      if (threadIdx.x == 0 && b == 0 && d0 == 0) flag = 0;
-      f32x4 *mine = reinterpret_cast<f32x4 *>(lds + wave * F::kEach) + hf * 32 + n;
+    for (int x = 0; x < D / 8; ++x) {                     // x = 4 db + g: d = 8 x + 4 hf ..
+      const f32x16 &y = o[b][x / 4];
+      mine[x * 64] = f32x4{y[4 * (x % 4)], y[4 * (x % 4) + 1], y[4 * (x % 4) + 2], y[4 * (x % 4) + 3]};
+    }
+    if (hf == 0) jm[wave][n] = make_float2(m[b], total);
+    __syncthreads();
+    if (PAGED && P.status && bad) flag = 1;
+    constexpr int kMine = D / 8 / F::kKW;                 // quads of this wave
+    float2 ml[F::kKW];
+    float top = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < F::kJoinD / 8; ++x) {           // x = 4 db + g: d = d0 + 8 x + 4 hf ..
-        const f32x16 &y = o[b][d0 / 32 + x / 4];
-        mine[x * 64] = f32x4{y[4 * (x % 4)], y[4 * (x % 4) + 1], y[4 * (x % 4) + 2], y[4 * (x % 4) + 3]};
-      }
-      if (hf == 0 && d0 == 0) jm[wave][n] = make_float2(m[b], total);
-      __syncthreads();
-      if (PAGED && P.status && bad) flag = 1;
-      constexpr int kMine = D / 8 / F::kKW;               // quads of this wave
-      const int at = kw * kMine * 8 - d0;                 // where they start in what is here
-      if (at < 0 || at >= F::kJoinD) continue;
-      float2 ml[F::kKW];
-      float top = -INFINITY;
+    for (int k = 0; k < F::kKW; ++k) {
+      ml[k] = jm[k * RW + rw][n];
+      top = fmaxf(top, ml[k].x);
+    }
+    const float to = top == -INFINITY ? 0.0f : top;
+    Done<D, F::kKW> R;
+    R.m = top;
+    R.l = 0.0f;
 #pragma unroll
-      for (int k = 0; k < F::kKW; ++k) {
-        ml[k] = jm[k * RW + rw][n];
-        top = fmaxf(top, ml[k].x);
-      }
-      const float to = top == -INFINITY ? 0.0f : top;
-      R.m = top;
-      R.l = 0.0f;
+    for (int i = 0; i < kMine; ++i) R.o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) R.o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < F::kKW; ++k) {
+      const float f = __builtin_amdgcn_exp2f((ml[k].x - to) * sl);
+      R.l = fmaf(ml[k].y, f, R.l);
+      const f32x4 *of = reinterpret_cast<const f32x4 *>(lds + (k * RW + rw) * F::kEach) + hf * 32 + n + kw * kMine * 64;
 #pragma unroll
-      for (int k = 0; k < F::kKW; ++k) {
-        const float f = __builtin_amdgcn_exp2f((ml[k].x - to) * sl);
-        R.l = fmaf(ml[k].y, f, R.l);
-        const f32x4 *of = reinterpret_cast<const f32x4 *>(lds + (k * RW + rw) * F::kEach) + hf * 32 + n + at / 8 * 64;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) R.o[i] += of[i * 64] * f;
-      }
+      for (int i = 0; i < kMine; ++i) R.o[i] += of[i * 64] * f;
     }
     const int side = QB == 1 ? rw : b;
     R.mine = J.row0 + side * 32 + n < rows;

@@ -38,8 +38,6 @@ inline int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Workgroups that join `rows` query rows: a wave each.
 inline long long join_grid(long long rows) { return (rows + kThreads / kWave - 1) / (kThreads / kWave); }
 
-constexpr int kWholeRows = 1024;
-
 // How a call is cut: waves side by side, row tiles, pieces aimed at; few: by few_kernel.
 struct Plan {
   bool few;
@@ -59,8 +57,7 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
     p.rw = R > 32 ? 2 : 1;
     p.kt = 32;
   }
-  const bool pairs = p.few && p.rw == 2 && dt == SPEC_BF16 && D <= 128;        // two blocks of query rows in a wave
-  p.threads = p.few && D <= 128 && !pairs ? 2 * kThreads : kThreads;
+  p.threads = p.few && D <= 128 ? 2 * kThreads : kThreads;
   p.row_tiles = static_cast<int>((R + 32 * p.rw - 1) / (32 * p.rw));
   p.groups = static_cast<long long>(B) * H * p.row_tiles;
   p.tiles = p.groups * ((max_rows + p.kt - 1) / p.kt);
@@ -68,15 +65,24 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   // a row takes up to 256 bytes and a workgroup more than 32 query rows.  (512 for
   // all: 66-node float32 trees, 28 heads of 128, took 46 us instead of 37.)  The
   // kernels of bf16 heads up to 64 would fit once more on a CU than this counts.
-  p.target = (p.few ? pairs : p.rw > 1 && row <= 256) ? 512 : 256;
+  p.target = !p.few && p.rw > 1 && row <= 256 ? 512 : 256;
   p.slots = p.groups + (p.tiles < p.target ? p.tiles : p.target);
   if (p.few) {
-    // Not cut at all, and so not joined: where the groups alone fill the chip, or where
-    // a group's longest walk takes no longer than the second launch.
-    if (p.groups >= p.target || max_rows <= kWholeRows) p.target = 0;
-    // the kernel's second look keeps up to 64 sequences' pieces to the target
-    if (p.target == 0) p.slots = p.groups;
-    else if (B <= kWave) p.slots = p.target;
+    // Not cut at all, and so not joined, where a cut would save less than it costs, counted
+    // in turns of a workgroup's waves over the cache's rows: the second launch is five
+    // turns (one token over 1100 rows takes 11.1 us in one launch, 12.7 in two). Groups
+    // that fill the chip gain by a cut only if their lengths differ: sequences of 64 ..
+    // 8192 rows take 81 us in one launch and 90 in two, one of 8192 rows beside 31 of 64
+    // takes 73 and 32, so a quarter of the longest walk counts as what a cut may save.
+    const bool bf = dt == SPEC_BF16;
+    const long long turn = 32 * (p.threads / kWave) / (p.rw == 2 && !(bf && D <= 128) ? 2 : 1);   // cache rows
+    const long long idle = p.target - p.groups > p.target / 4 ? p.target - p.groups : p.target / 4;
+    if (max_rows * idle <= 5 * turn * p.target) {
+      p.target = 0;
+      p.slots = p.groups;
+    } else if (B <= kWave && 2 * p.groups <= p.target) {
+      p.slots = p.target;                                 // as the kernel's second look sees to
+    }
   }
   if (p.slots > p.tiles) p.slots = p.tiles;
   return p;
@@ -122,8 +128,9 @@ __device__ inline int tree_tiles(const Params &P, int n, int E, int kt) {
 }
 
 // What a workgroup does: finds its piece, walks it by `walk` and stores the results.
-// KT: rows of a tile that pieces are counted in; KW: waves behind each other.
-template <typename T, int DP, int RW, bool PAGED, int KT, int KW, class Walk>
+// KT: rows of a tile that pieces are counted in; KW: waves behind each other; LOOK: the
+// second look is taken for groups of up to 1 / LOOK of the target.
+template <typename T, int DP, int RW, bool PAGED, int KT, int KW, int LOOK, class Walk>
 __device__ inline void tree_piece(const Params &P, Walk walk) {
   const int lane = threadIdx.x & (kWave - 1);
   const int H = P.c.H, each = H * P.row_tiles, E = PAGED ? 0 : *P.c.end_col;
@@ -137,11 +144,12 @@ __device__ inline void tree_piece(const Params &P, Walk walk) {
   // few workgroups more than that would run alone behind all the others: 16-node
   // trees over 32 sequences of 512 .. 4096 rows took 74 us so and 84 us without
   // the second look, 255-node trees over 32k rows 324 and 410 us.  It is not taken
-  // for more than 64 sequences, nor where the groups alone exceed the target.
+  // for more than 64 sequences, nor where the groups alone exceed the target (or, over
+  // 4-bit numbers, where the few pieces left would cut nothing: half the target).
   const bool whole = P.target == 0;                       // no group is cut
   int per = whole ? INT32_MAX : max(1, (total + P.target - 1) / P.target);
   auto pieces_of = [&](int tiles) { return whole ? min(tiles, 1) : (tiles + per - 1) / per; };
-  if (P.B <= kWave && each * P.B <= P.target)
+  if (P.B <= kWave && each * P.B * LOOK <= P.target)
     while (per > 1 && wave_reduce(pieces_of(tiles0), [](int a, int c) { return a + c; }) * each > P.target)
       per += (per + 15) / 16;
   // this workgroup's sequence: the pieces are numbered in the order of sequence, head, row tile
@@ -219,7 +227,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 && sizeof(T) == 2 && RW > 1 ? 2
   using S = Shape<T, DP, RW>;
   __shared__ __attribute__((aligned(16))) char buf0[S::kLds];
   __shared__ __attribute__((aligned(16))) char buf1[S::kLds];
-  tree_piece<T, DP, RW, PAGED, S::kKT, S::kKW>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
+  tree_piece<T, DP, RW, PAGED, S::kKT, S::kKW, 1>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
     Done<DP, S::kKW> D;
     const bool bad = walk<T, DP, RW, PAGED, false, ONCE, MX>(P, J, D, buf0, buf1);
     store(D, __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % RW, sees_any(P, J.b, D.token));
@@ -232,7 +240,7 @@ template <typename T, int D, int RW, int QB, bool PAGED>
 __global__ __launch_bounds__((Few<T, D, RW, QB>::kThreads), D <= 128 ? 2 : 1) void few_kernel(Params P) {
   using F = Few<T, D, RW, QB>;
   __shared__ __attribute__((aligned(16))) char lds[F::kLds];
-  tree_piece<T, D, RW * QB, PAGED, 32, F::kKW>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
+  tree_piece<T, D, RW * QB, PAGED, 32, F::kKW, 2>(P, [&](const Job &J, auto store) __attribute__((always_inline)) {
     return few_walk<T, D, RW, QB, PAGED>(P, J, store, lds);
   });
 }

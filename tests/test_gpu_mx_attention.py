@@ -108,6 +108,26 @@ def test_many_sequences():
     _check(22, "f32", rng.integers(0, 90, 70), 3, 2, 1, 64, 8, "any", L=1)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,N,G,D,page,longest", [
+    (64, 5, 2, 2, 64, 16, 6500),                         # more groups than workgroups, cut
+    (60, 3, 16, 4, 128, 32, 6100),                       # groups for over half of the workgroups, cut
+    (70, 1, 1, 3, 128, 16, 5400),                        # more sequences than lanes
+    (30, 5, 9, 4, 64, 0, 700), (90, 3, 12, 5, 128, 8, 300)])   # one launch, below and above the chip's workgroups
+def test_one_long_sequence_among_many(dt, B, H, N, G, D, page, longest):
+    rng = np.random.default_rng(B)
+    n = rng.integers(0, 40, B)
+    n[B // 3], n[B // 2] = longest, 0
+    _check(B, dt, n, N, H, G, D, page, "chain", L=1)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,G", [(8, 4), (11, 3), (16, 4), (13, 5), (64, 1), (65, 1)])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_around_32_and_64_query_rows(dt, N, G, D):
+    _check(N * G + D, dt, [257, 30], N, 2, G, D, 0, "tree", L=1)
+
+
 def test_sharp_scores_and_scales():
     _check(5, "bf16", [200, 31], 8, 2, 4, 128, 0, "tree", sd=60.0)      # scores of several hundreds
     _check(6, "f32", [200, 31], 8, 2, 4, 64, 16, "tree", sd=60.0)

@@ -473,7 +473,7 @@ def _mx_dims(codes, scales, heads: int):
     """As _cache_dims, of a cache of 4-bit numbers: codes [L, 2, planes, H, cols, D / 2] and scales
     [L, 2, planes, H, cols, D / 32], uint8."""
     L, planes, H, cols, half, G = _cache_dims(codes, heads)
-    if tuple(scales.shape) != tuple(codes.shape[:5]) + (half // 16,) or half % 32:
+    if half < 32 or half % 32 or scales.shape != (L, 2, planes, H, cols, half // 16):
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)}: D / 2 and D / 32 of a D that "
                          "is a multiple of 64 are needed")
     return L, planes, H, cols, 2 * half, G
@@ -482,11 +482,15 @@ def _mx_dims(codes, scales, heads: int):
 def _cache_at(kv, scales, heads: int, stream):
     """A call's cache: its sizes as _cache_dims gives them, its device and stream, and its address, or those
     of a cache of 4-bit numbers' codes and scales."""
-    dims = _cache_dims(kv, heads) if scales is None else _mx_dims(kv, scales, heads)
-    dev, s = _place(kv, stream)
     if scales is None:
+        dims = _cache_dims(kv, heads)
+        dev, s = _place(kv, stream)
         return dims, dev, s, (kv.data_ptr(),)
-    return dims, dev, s, (_need(kv, torch.uint8, 0, "codes", dev), _need(scales, torch.uint8, 0, "scales", dev))
+    dims = _mx_dims(kv, scales, heads)                      # that codes are contiguous is seen there
+    dev, s = _place(kv, stream)
+    if kv.dtype is not torch.uint8:
+        raise ValueError(f"codes must be torch.uint8, not {kv.dtype}")
+    return dims, dev, s, (kv.data_ptr(), _need(scales, torch.uint8, 0, "scales", dev))
 
 
 def _norm_rope(name, paged, q, k, v, kv, layer, where, kv_len, q_out, cu_seqlens, positions, q_weight, k_weight, eps,
@@ -632,9 +636,9 @@ def _unpack(name, paged, codes, scales, layer, where, kv_len, k_out, v_out, cu_s
     (L, planes, H, cols, D, _), dev, s, cache = _cache_at(codes, scales, codes.shape[3], stream)
     i32 = torch.int32
     B = where.shape[0] if paged else planes
-    if k_out.numel() % (H * D) or not k_out.numel():
+    T, left = divmod(k_out.numel(), H * D)
+    if left or not T:
         raise ValueError(f"k_out must hold [T, {H}, {D}] elements, has {k_out.numel()}")
-    T = k_out.numel() // (H * D)
     if cu_seqlens is None and (B < 1 or T % B):
         raise ValueError(f"{T} tokens are no whole number for each of {B} sequences")
     N = T // B if cu_seqlens is None else 0

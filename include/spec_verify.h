@@ -717,6 +717,10 @@ int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool,
  *   dt           the type of q, k, v, weights and outputs; the cache has none
  *   D            a multiple of 64, at most SPEC_ATTN_MAX_D
  *   codes, scales  multiples of 16 bytes; they may not overlap each other
+ *   work-items   trees with N * G of at most 64: 512 for each of the workgroups that
+ *                those of up to 64 query rows need
+ *   between batches, trees with N * G of at most 64: whether a sequence's rows are cut
+ *                at all follows B, H and the capacity (C, or max_pages * page_size)
  *
  * spec_norm_rope_kv_mx -- as spec_norm_rope_kv; keys (computed in float64 from
  * their inputs, so that which code an element gets is a matter of its value and not

@@ -25,6 +25,9 @@
 // over 25k and 33k rows: 287 us = 840 TFLOP/s (there the matrix units bound, as in
 // prompts); five tokens of 8 sequences of 64 .. 2048 rows in pages, 28 heads over
 // 4: 18 us; one token over 1100 rows: 12 us, the latency of two launches.
+// Over 4-bit numbers up to 64 query rows go the way of few_rows.h, in one launch where a
+// cut would not pay; more of them take the tiles, filled by conversion: the 255-node trees
+// over 25k and 33k rows take 264 us = 916 TFLOP/s.
 #pragma once
 
 #include "few_rows.h"

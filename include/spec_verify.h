@@ -760,7 +760,7 @@ int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool,
  * Errors: SPEC_EINVAL for NULL required pointers, sizes < 1, misalignment, overlap,
  * max_pages * page_size above 2^31 - 513, counts of 2^31 and more, more than
  * 2^32 - 1 work-items (256 for each sequence, layer, K/V and, where those are fewer
- * than 2048, group of heads); SPEC_ECAPACITY for N > SPEC_TREE_MAX_N.
+ * than 1024, group of heads); SPEC_ECAPACITY for N > SPEC_TREE_MAX_N.
  * ------------------------------------------------------------------------ */
 int spec_norm_rope_kv_mx(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                          int64_t v_stride, uint8_t *codes, uint8_t *scales, spec_dtype dt, int L, int B,

@@ -14,7 +14,7 @@
 // path and its pages in one round of loads with a lane per slot, leaves the slots'
 // offsets in LDS, and moves units of up to 16 bytes.
 // Measured: 32 trees of 63 nodes with 2 .. 24 kept, 28 layers of 4 heads of 128 in bf16
-// (45 MB read and written) 13.6 us = 3.3 TB/s, two dependent rounds of loads before the
+// (45 MB read and written) 13.5 us = 3.3 TB/s, two dependent rounds of loads before the
 // first row moves; one tree of 16 nodes, 32 layers of 8 heads, 3.6 us.
 #include <algorithm>
 
@@ -119,10 +119,11 @@ extern "C" int spec_compact_tree_paged(void *pool, spec_dtype dt, int L, int pag
   // units of a workgroup and a row's bytes in 31 bits
   if (R > INT32_MAX / SPEC_TREE_MAX_N || static_cast<long long>(H) * N * R >= INT32_MAX) return SPEC_EINVAL;
   if (static_cast<long long>(L) * B >= INT32_MAX / 2) return SPEC_EINVAL;
-  // enough workgroups to fill the chip: each sequence's heads are split where its
-  // layers alone are too few
+  // four workgroups a CU: each sequence's heads are split where its layers alone are too
+  // few (32 trees, 28 layers: 1792 workgroups of 4 heads take 13.3 us, twice as many of 2
+  // heads 14.1, since each has the path to look up first)
   const long long groups = static_cast<long long>(B) * 2 * L;
-  const int split = static_cast<int>(std::min<long long>(H, std::max<long long>(1, (2048 + groups - 1) / groups)));
+  const int split = static_cast<int>(std::min<long long>(H, std::max<long long>(1, (1024 + groups - 1) / groups)));
   P.hpb = (H + split - 1) / split;
   P.hsplit = (H + P.hpb - 1) / P.hpb;
   if (!launchable(groups * P.hsplit, kThreads)) return SPEC_EINVAL;

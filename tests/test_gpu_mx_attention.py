@@ -250,6 +250,69 @@ def test_calls_repeat_bit_for_bit_on_streams_and_in_graphs():
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,G", [(3, 2), (16, 4), (40, 4)])
+def test_bad_sequences_beside_one_that_is_cut(dt, N, G):
+    """A long cache in pieces: one page of it is missing, and of its neighbours one has no length, one no room."""
+    rng = np.random.default_rng(43)
+    n = np.array([6500, 25, 60, 40])
+    cache = MxCache(rng, dt, 1, 2, 128, n + N, n, 32)
+    q = randn(rng, dt, 4 * N, 2 * G, 128)
+    see = _see(rng, "chain", 4, N)
+    want, want_l, tol, tol_l = attend_all(q, cache, 0, [N] * 4, _whole(see, n), 1.0 / np.sqrt(128))
+    kv, qd = cache.on_device(), dev(q).view(4, N, 2 * G, 128)
+    said, table = n.copy(), cache.table.copy()
+    said[1], said[2] = -1, cache.max_rows()
+    note(f"mx bad sequences, cut {dt} N={N}")
+    for page, status in ((None, 0), (150, 16)):
+        if page is not None:
+            table[0, page] = -1
+        out, l, st = _tree(qd, cache, kv, 0, said, None, 4, N, where=i32(table))
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == [status, 16, 32, 0]
+        for b in (1, 2):
+            assert bool((out[b] == 0).all()) and bool((l[b] == float("-inf")).all())
+        for b in (0, 3) if page is None else (3,):
+            at = slice(b * N, (b + 1) * N)
+            shape = (4 * N, 2 * G, 128)
+            assert_within(out[b], want.reshape(shape)[at], tol.reshape(shape)[at], f"out {b}")
+            assert_within(l[b], want_l.reshape(shape[:2])[at], tol_l.reshape(shape[:2])[at], f"lse {b}")
+        assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_cut_call_repeats_on_streams_and_in_graphs(dt):
+    rng = np.random.default_rng(52)
+    n, N = np.array([7000, 40, 3333]), 5
+    cache = MxCache(rng, dt, 1, 2, 128, n + N, n, 64)
+    q = dev(randn(rng, dt, 3, N, 8, 128))
+    kv, where = cache.on_device(), cache.where()
+    need = sv.spec_tree_attention_mx_workspace_bytes(3, N, 2, 4, 128, cache.max_rows(),
+                                                     sv.SPEC_BF16 if dt == "bf16" else sv.SPEC_F32)
+    nd, side = i32(n), torch.cuda.Stream()
+    note(f"mx cut tree repeats {dt}")
+    first, _, _ = _tree(q, cache, kv, 0, n, None, 3, N)
+    outs, spaces = ([make() for _ in range(2)] for make in (lambda: torch.empty_like(first), lambda: sv.workspace(need, DEV)))
+    torch.cuda.synchronize()
+    for i, stream in enumerate((side, None)):
+        sv.spec_tree_attention_mx_paged(q, *kv, 0, where, nd, outs[i], spaces[i], stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(first, outs[0]) and torch.equal(first, outs[1])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]   # of one workspace, replayed one after the other
+    for graph, out in zip(graphs, outs):
+        with torch.cuda.graph(graph):
+            sv.spec_tree_attention_mx_paged(q, *kv, 0, where, nd, out, spaces[0])
+    for lens in ([7000, 40, 3333], [10, 0, 3000], [6999, 39, 1], [7000, 40, 3333]):
+        nd.copy_(i32(lens))
+        want, _, _ = _tree(q, cache, kv, 0, np.array(lens), None, 3, N)
+        for out in outs:
+            out.fill_(3.0)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 # ------------------------------------------------------------------- prompts ----
 def _prompt(q, cache, kv, layer, cu, n, scale=None, stream=None):
     B, T, Hq = len(n), q.shape[0], q.shape[1]

@@ -717,8 +717,8 @@ int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool,
  *   dt           the type of q, k, v, weights and outputs; the cache has none
  *   D            a multiple of 64, at most SPEC_ATTN_MAX_D
  *   codes, scales  multiples of 16 bytes; they may not overlap each other
- *   work-items   trees with N * G of at most 64: 512 for each of the workgroups that
- *                those of up to 64 query rows need
+ *   work-items   trees with N * G of at most 64: 512 (D > 128: 256) for each KV head of
+ *                a sequence, and as many for up to 256 pieces more of long caches
  *   between batches, trees with N * G of at most 64: whether a sequence's rows are cut
  *                at all follows B, H and the capacity (C, or max_pages * page_size)
  *

@@ -153,14 +153,9 @@ __device__ inline void key_turned(const RopeParams &P, u32x4 x, const T *src, in
   for (int j = 0; j < kN; ++j) {
     const Turn t = turn_at<PAIRS>(P.half, e0, j);
     const double2 angle = angles[t.pair];
-    double p, o;
-    if constexpr (sizeof(T) == 2) {                       // products of bf16 are exact in float32
-      p = a[j] * w[0][j];
-      o = m[j] * w[1][j];
-    } else {
-      p = static_cast<double>(a[j]) * w[0][j];
-      o = static_cast<double>(m[j]) * w[1][j];
-    }
+    // in float64: the fraction of a product of bf16 would fit float32, its exponent need not (2^100 times
+    // 2^30, while the normed key is 2^30); 20.9k tokens of 32 + 16 heads of 128 take 115 us so, 110 otherwise
+    const double p = static_cast<double>(a[j]) * w[0][j], o = static_cast<double>(m[j]) * w[1][j];
     y[j] = mx_sided((t.in ? fma(o, t.low ? -angle.x : angle.x, p * angle.y) : p) * r);
   }
 }

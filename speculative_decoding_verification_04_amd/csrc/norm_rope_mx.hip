@@ -22,6 +22,20 @@ namespace {
 constexpr int kWaves = kMaxThreads / kWave;
 constexpr int kU = 4;          // blocks of query heads in flight
 
+// pos * freq in turns of the circle, less the nearest whole number of them: off by the
+// rounding of the last sum, 2^-54 of a turn, at any position.  The product's rounding and
+// 1 / (2 pi)'s second half are carried along, and nothing may be contracted: turn -
+// rint(turn) as one fma would hold the rounding of turn, which rest adds (so contracted,
+// position 2000 was off by 2^-46 of a turn and 2^31 - 1 by 2^-26).
+__device__ inline double turns_of(int pos, float freq) {
+#pragma clang fp contract(off)
+  const double p = pos, f = freq, angle = p * f, low = fma(p, f, -angle);
+  const double turn = angle * 0.15915494309189533577;
+  const double rest = fma(angle, 0.15915494309189533577, -turn) +
+                      (angle * -9.839338337591243e-18 + low * 0.15915494309189533577);
+  return (turn - rint(turn)) + rest;
+}
+
 // Sine and cosine of t turns of the circle, t within [-1/2, 1/2]: their series on an
 // eighth of the circle, within 2^-52.
 __device__ inline double2 turn_of(double t) {
@@ -251,10 +265,7 @@ __global__ __launch_bounds__(kMaxThreads, 4) void norm_rope_mx_kernel(RopeParams
   if (place.at == kNoSequence) return;
   const int pos = P.positions ? given : place.row;
   for (int i = lane; i < half; i += kWave) {
-    const double angle = static_cast<double>(pos) * (i < kWave ? freq : P.inv_freq[i]), turn = angle * 0.15915494309189533577;
-    // 1 / (2 pi) in two parts, and the product's own rounding: far positions keep 2^-52 of a turn
-    const double rest = fma(angle, 0.15915494309189533577, -turn) + angle * -9.839338337591243e-18;
-    angles[i] = turn_of(turn - rint(turn) + rest);
+    angles[i] = turn_of(turns_of(pos, i < kWave ? freq : P.inv_freq[i]));
   }
   __builtin_amdgcn_wave_barrier();                        // the wave's own LDS, in order
 #pragma unroll

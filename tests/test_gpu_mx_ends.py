@@ -1,5 +1,8 @@
 """Writing rows into a cache of 4-bit numbers where exponents and angles leave the
-ordinary."""
+ordinary: sizes of keys and weights, positions far from 0."""
+from fractions import Fraction
+from functools import cache
+
 import numpy as np
 import pytest
 import torch
@@ -57,3 +60,60 @@ def test_sizes_of_keys_and_weights(dt, rot, near, key, weight, eps):
     want_c, want_s = mx.pack(want)
     assert np.array_equal(s[0], want_s)
     assert np.array_equal(c[0], want_c)
+
+PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679, 10 ** 100)
+
+
+def _turned(pos, freq):
+    """Cosine and sine of pos * freq: the angle is reduced exactly, so they are float64's nearest but for 2^-52."""
+    turns = Fraction(int(pos)) * Fraction(float(freq)) / (2 * PI)
+    t = float((turns - round(turns)) * 2 * PI)
+    return np.cos(t), np.sin(t)
+
+
+@cache
+def _cases(pos, freq):
+    """(border, side, pair) for keys that turn by pos * freq, and that angle's cosine and sine."""
+    rng = np.random.default_rng(pos % 1000)
+    cos, sin = _turned(pos, freq)
+    cases = [(b, side, _pair_next_to(rng, b, cos, sin, side)) for b in (0.75, 1.25, 1.75, 2.5, 3.5) for side in (-1, 1)]
+    return [x for x in cases if x[2]], cos, sin
+
+
+def _pair_next_to(rng, border, cos, sin, side):
+    """float32 a and m with a cos - m sin between 2^-44 and 2^-42 from the border, on the given side."""
+    other = rng.uniform(2.0, 5.8, 1 << 22)                # its partner: what an error of the angle is multiplied by
+    a = (border * cos + other * sin).astype(np.float32).astype(np.float64)
+    m = ((a * cos - border) / sin).astype(np.float32).astype(np.float64)
+    off = (a * cos - m * sin - border) * side
+    good = np.nonzero((off > 2.0 ** -44) & (off < 2.0 ** -42) & (np.abs(m * cos + a * sin) < 5.9))[0]
+    return (a[good[0]], m[good[0]]) if len(good) else None
+
+
+@pytest.mark.parametrize("rot,near", [(64, False), (2, False), (64, True)])
+@pytest.mark.parametrize("pos,freq", [(1, 1.0), (2000, 1.0), (2000, 0.7), (131071, 1.0), (131071, 0.9), ((1 << 20) + 1, 0.7),
+                                      ((1 << 24) + 3, 0.3), ((1 << 29) + 1, 0.9), (2 ** 31 - 1, 1.0), (2 ** 31 - 1, 0.7)])
+def test_angles_decide_no_code(pos, freq, rot, near):
+    """Keys whose rotated element lies 2^-44 to 2^-42 from a border, on either side.  An angle that is off by
+    2^-54 of a turn moves it by 2 pi 2^-54 times its partner (below 6), and the sine, the cosine and the products
+    by 2^-49 at most: 2^-48 together."""
+    note(f"mx angles pos={pos} freq={freq} rot={rot} near={near}")
+    freq = np.float32(freq)
+    cases, cos, sin = _cases(pos, freq)
+    assert len(cases) >= 4
+    D, half = 64, rot // 2
+    T, lo, hi = len(cases), 0, 1 if near else half
+    k = np.zeros((T, 1, D), np.float32)
+    want = np.zeros((T, 1, D))
+    still = 10 if rot > 2 else 4                          # a pair that does not turn, in both blocks: the largest elements
+    k[:, 0, still] = k[:, 0, still + 32] = want[:, 0, still] = want[:, 0, still + 32] = 6.0
+    for t, (border, side, (a, m)) in enumerate(cases):
+        k[t, 0, lo], k[t, 0, hi] = a, m
+        want[t, 0, lo], want[t, 0, hi] = a * cos - m * sin, m * cos + a * sin
+    inv_freq = np.zeros(half, np.float32)
+    inv_freq[0] = freq
+    x = torch.from_numpy(k)
+    c, s, _ = _write(x, x, x, positions=[pos] * T, inv_freq=torch.from_numpy(inv_freq), interleaved=near)
+    want_c, want_s = mx.pack(want)
+    assert np.array_equal(s[0], want_s)
+    assert np.array_equal(c[0], want_c), [x[:2] for x, g, w in zip(cases, c[0], want_c) if not np.array_equal(g, w)]

@@ -100,15 +100,16 @@ __device__ inline uint32_t mx_codes_bf16(const uint32_t (&x)[4], int byte) {
 
 // A double as the float on its way to a code: cut to 20 bits of its fraction, with the
 // last of them set where anything was cut off, so that it is on the double's side of
-// every border (borders have few bits).  Past float32's range: infinity; between half
-// and all of the smallest normal number, three quarters of it, and 0 below.
+// every border (borders have few bits).  What float32 would round to infinity, from
+// 2^128 - 2^103 on: infinity; between half and all of the smallest normal number, three
+// quarters of it, and 0 below.
 __device__ inline float mx_sided(double x) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t high = static_cast<uint32_t>(u >> 32), size = (high & 0x7fffffffu) | (static_cast<uint32_t>(u) ? 1u : 0u);
   const uint32_t base = 896u << 20;                       // what exponents differ by
   uint32_t bits = (size - base) << 3;
   if (size < base + (1u << 20)) bits = size > base ? 0x00600000u : 0u;
-  if (size >= base + (255u << 20)) bits = size > 0x7ff00000u ? 0x7fc00000u : 0x7f800000u;
+  if (!(fabs(x) < 0x1.ffffffp127)) bits = size > 0x7ff00000u ? 0x7fc00000u : 0x7f800000u;
   return __uint_as_float(bits | (high & 0x80000000u));
 }
 

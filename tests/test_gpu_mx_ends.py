@@ -1,5 +1,5 @@
 """Writing rows into a cache of 4-bit numbers where exponents and angles leave the
-ordinary: sizes of keys and weights, positions far from 0."""
+ordinary: sizes of keys and weights, positions far from 0, the largest numbers."""
 from fractions import Fraction
 from functools import cache
 
@@ -117,3 +117,21 @@ def test_angles_decide_no_code(pos, freq, rot, near):
     want_c, want_s = mx.pack(want)
     assert np.array_equal(s[0], want_s)
     assert np.array_equal(c[0], want_c), [x[:2] for x, g, w in zip(cases, c[0], want_c) if not np.array_equal(g, w)]
+
+
+def test_keys_next_to_the_largest_number():
+    """As float32 a key of 2^128 - 2^103 and more is infinite, and one below it the largest number."""
+    note("mx largest keys")
+    largest, t = float(np.finfo(np.float32).max), 2.0 ** -20
+    k = np.zeros((5, 1, 64), np.float32)
+    for i, steps in enumerate((0.0, 0.9, 0.99, 1.01, 1.5)):   # of 2^103 above the largest number
+        k[i, 0, 0], k[i, 0, 32] = largest, -steps * 2.0 ** 103 / t
+    freq = np.zeros(32, np.float32)
+    freq[0] = t
+    want = oracle.norm_rope(k.astype(np.float64), None, 0.0, [1] * 5, freq)
+    x = torch.from_numpy(k)
+    c, s, _ = _write(x, x, x, positions=[1] * 5, inv_freq=torch.from_numpy(freq))
+    want_c, want_s = mx.pack(want)
+    assert want_s[:, 0, 0].tolist() == [252, 252, 252, 255, 255]
+    assert np.array_equal(s[0], want_s)
+    assert np.array_equal(c[0], want_c)

@@ -121,24 +121,32 @@ __device__ inline void weights_of(const void *weights, int half, int e0, bool ac
   }
 }
 
-// A lane's elements of a query after norm and rotation: (a c + m s) r, with c and s the
-// cosine and the signed sine times the weights.
+// A lane's elements of a query after norm and rotation: r a c + r m s, with c and s the
+// cosine and the signed sine times the weights.  The norm comes first: an element times
+// its weight may leave float32 where the result does not.
 template <typename T, Pairs PAIRS>
 __device__ inline void query_turned(const RopeParams &P, u32x4 x, const T *src, int e0, bool active,
                                     const float (&c)[Vec<T>::n], const float (&s)[Vec<T>::n], float (&y)[Vec<T>::n]) {
   constexpr int kN = Vec<T>::n;
-  float a[kN], m[kN], r = 1.0f;
+  float a[kN], m[kN];
   with_mates<T, PAIRS>(x, src, P.half, e0, active, a, m);
   if (P.q_weight) {
     float squares = 0.0f;
 #pragma unroll
     for (int j = 0; j < kN; ++j) squares = fmaf(a[j], a[j], squares);
-    r = __builtin_amdgcn_rsqf(group_sum(squares, P.lanes) / static_cast<float>(P.c.D) + P.eps);
+    const float of = group_sum(squares, P.lanes) / static_cast<float>(P.c.D) + P.eps;
+    const bool low = of < 0x1p-100f;                      // the instruction takes what is no normal number for 0
+    const float r = __builtin_amdgcn_rsqf(low ? of * 0x1p64f : of) * (low ? 0x1p32f : 1.0f);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      a[j] *= r;
+      m[j] *= r;
+    }
   }
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
     const float z = a[j] * c[j];
-    y[j] = (turn_at<PAIRS>(P.half, e0, j).in ? fmaf(m[j], s[j], z) : z) * r;
+    y[j] = turn_at<PAIRS>(P.half, e0, j).in ? fmaf(m[j], s[j], z) : z;
   }
 }
 

@@ -1,5 +1,5 @@
 """Writing rows into a cache of 4-bit numbers where exponents and angles leave the
-ordinary: sizes of keys and weights, positions far from 0, the largest numbers."""
+ordinary: sizes of keys, queries and weights, positions far from 0, the largest numbers."""
 from fractions import Fraction
 from functools import cache
 
@@ -10,7 +10,7 @@ import torch
 import oracle
 import speculative_decoding_verification_04_amd as sv
 from oracle import mx
-from tests._attn import dev, f64, randn
+from tests._attn import EPS32, HALF, assert_within, dev, f64, randn
 from tests._gpu import DEV, i32, note, requires_gpu
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
@@ -135,3 +135,25 @@ def test_keys_next_to_the_largest_number():
     assert want_s[:, 0, 0].tolist() == [252, 252, 252, 255, 255]
     assert np.array_equal(s[0], want_s)
     assert np.array_equal(c[0], want_c)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rot,near", [(0, False), (64, False), (22, False), (64, True)])
+@pytest.mark.parametrize("query,weight,eps", [(50, 90, 1e-5), (-50, -90, 0.0), (-50, 110, 0.0), (-64, 0, 0.0), (-64, 100, 0.0),
+                                              (40, -110, 1e-6)])
+def test_sizes_of_queries_and_weights(dt, rot, near, query, weight, eps):
+    """As spec_norm_rope_kv's queries: statistics in float32, the norm before the weight.  Squares of 2^-64 are
+    below the smallest normal number and off by 2^-150 each, 2^-22 of themselves, and the root by half of it:
+    two EPS32 more."""
+    note(f"mx sizes of queries {dt} rot={rot} near={near} 2^{query} 2^{weight}")
+    rng = np.random.default_rng(abs(query) + rot)
+    T, Hq, H, D = 6, 6, 3, 64
+    q, kv = _times(randn(rng, dt, T, Hq, D), query), randn(rng, dt, T, H, D)
+    w = _times(randn(rng, dt, D), weight)
+    want = oracle.norm_rope(f64(q), f64(w), eps, np.arange(T), _freq(rot // 2), near)
+    size = np.abs(oracle.norm_rope(f64(q), f64(w), eps, np.arange(T), _freq(0), near)).max(-1, keepdims=True)
+    _, _, got = _write(q, kv, kv, q_weight=w, eps=eps, interleaved=near,
+                       inv_freq=torch.from_numpy(_freq(rot // 2)) if rot else None)
+    # results below the smallest normal number have an absolute step, 2^-133 in bf16
+    tol = (D + 34) * EPS32 * size + 1.01 * HALF[dt] * np.abs(want) + 2.0 ** (-133 if dt == "bf16" else -149)
+    assert_within(got, want, tol)

@@ -157,3 +157,77 @@ def test_sizes_of_queries_and_weights(dt, rot, near, query, weight, eps):
     # results below the smallest normal number have an absolute step, 2^-133 in bf16
     tol = (D + 34) * EPS32 * size + 1.01 * HALF[dt] * np.abs(want) + 2.0 ** (-133 if dt == "bf16" else -149)
     assert_within(got, want, tol)
+
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,rot,near", [(64, 64, False), (128, 40, False), (192, 96, True), (256, 256, False)])
+def test_bytes_of_codes_and_scales(dt, D, rot, near):
+    """Every byte, signs of zeros and the codes of blocks that are not finite among them."""
+    note(f"mx bytes {dt} D={D} rot={rot} near={near}")
+    rng = np.random.default_rng(D)
+    T, H = 7, 3
+    k, v = randn(rng, dt, T, H, D, sd=3.0), randn(rng, dt, T, H, D, sd=3.0)
+    for x in (k, v):
+        x[0, 0, 5::7] = -0.0
+        x[2, 2, D - 1] = float("nan")
+        x[3, 0] = 0.0
+        x[4, 1] = -0.0
+        x[5, 2, 10:20] *= 2.0 ** -9                       # codes of 0 with either sign
+    v[1, 1, 3], v[1, 2, D - 1] = float("inf"), float("-inf")
+    w = randn(rng, dt, D)
+    with np.errstate(invalid="ignore"):
+        keys = oracle.norm_rope(f64(k), f64(w), 1e-5, np.arange(T), _freq(rot // 2), near)
+    c, s, _ = _write(randn(rng, dt, T, H, D), k, v, k_weight=w, eps=1e-5, interleaved=near,
+                     inv_freq=torch.from_numpy(_freq(rot // 2)))
+    for i, y in ((0, keys), (1, f64(v))):
+        want_c, want_s = mx.pack(y)
+        assert i == 1 or np.nanmin(mx.border_distance(y)) > 2.0 ** -36
+        assert np.array_equal(s[i], want_s), "kv"[i]
+        assert np.array_equal(c[i], want_c), "kv"[i]
+        assert (s[i] == 255).any() and (np.repeat(s[i] == 255, 16, axis=-1) <= (c[i] == 0)).all()
+
+
+def test_streams_and_replays_write_codes_and_scales():
+    """A call on another stream and each replay of a captured one fill the cache themselves."""
+    note("mx rows again")
+    rng = np.random.default_rng(16)
+    T, H, D = 5, 2, 128
+    q, k, v = (dev(randn(rng, "bf16", T, h, D)) for h in (4, H, H))
+    codes = torch.empty(1, 2, 1, H, 16, D // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(1, 2, 1, H, 16, D // 32, dtype=torch.uint8, device=DEV)
+    E, n, q_out = i32([4]), i32([3]), torch.empty_like(q)
+    rows = [codes, scales, q_out]
+
+    def write(stream=None):
+        sv.spec_norm_rope_kv_mx(q, k, v, codes, scales, 0, E, n, q_out, stream=stream)
+
+    def marked():
+        for x in rows:
+            x.view(torch.uint8).fill_(0x5A)
+
+    def result():
+        torch.cuda.synchronize()
+        return [x.clone() for x in rows]
+    marked()
+    write()
+    want = result()
+    assert int((want[0] != 0x5A).sum()) > 2 * H * T * D // 4 and int((want[1] != 0x5A).sum()) == 2 * H * T * D // 32
+    side = torch.cuda.Stream()
+    marked()
+    side.wait_stream(torch.cuda.current_stream())
+    write(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, result()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        write()
+    base = [x.clone() for x in (q, k, v)]
+    for i in range(4):
+        for x, y in zip((q, k, v), base):
+            x.copy_(y * (1 + i))
+        marked()
+        write()
+        want = result()
+        marked()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, result())), i

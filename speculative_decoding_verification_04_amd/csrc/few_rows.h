@@ -175,6 +175,8 @@ __device__ inline bool few_walk(const Params &P, const Job &J, Store store, char
         } else {
           const f32x4 a = reinterpret_cast<const f32x4 *>(at(i))[0], b4 = reinterpret_cast<const f32x4 *>(at(i))[1];
           float x[8] = {a[0], a[1], a[2], a[3], b4[0], b4[1], b4[2], b4[3]};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = x[k] == x[k] ? x[k] : NAN;   // a NaN's first part may be an infinity's
           q[0][i] = cut_part(x);
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = fabsf(x[k]) < INFINITY ? x[k] : 0.0f;   // infinity is its first part

@@ -24,7 +24,10 @@ constexpr int kMxBlock = 32, kMxNan = 255, kMxTop = 252;   // elements to a scal
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// Host checks of a cache of 4-bit numbers: as cache_view(); D a multiple of 64.
+inline size_t mx_rows(int L, int planes, int H, int cols) { return static_cast<size_t>(L) * 2 * planes * H * cols; }
+
+// Host checks of a cache of 4-bit numbers: as cache_view(); D a multiple of 64; codes and
+// scales apart.
 inline int mx_view(CacheView &c, const void *codes, const void *scales, int L, int planes, int H, int cols, int D,
                    int layer, const int32_t *table, int max_pages, bool paged, const int32_t *end_col,
                    const int32_t *kv_len) {
@@ -32,6 +35,8 @@ inline int mx_view(CacheView &c, const void *codes, const void *scales, int L, i
   const int err = cache_shape(c, L, planes, H, cols, D, layer, table, max_pages, paged, end_col, kv_len);
   if (err) return err;
   if (D % 64 || !aligned(codes, 16) || !aligned(scales, 16)) return SPEC_EINVAL;
+  const size_t all = mx_rows(L, planes, H, cols);
+  if (overlaps(codes, all * (D / 2), scales, all * (D / kMxBlock))) return SPEC_EINVAL;
   const long long rows = static_cast<long long>(planes) * H * cols;            // one layer's K
   c.k = static_cast<char *>(const_cast<void *>(codes)) + 2 * rows * (D / 2) * layer;
   c.v = c.k + rows * (D / 2);
@@ -39,8 +44,6 @@ inline int mx_view(CacheView &c, const void *codes, const void *scales, int L, i
   c.vs = c.ks + rows * (D / kMxBlock);
   return SPEC_OK;
 }
-
-inline size_t mx_rows(int L, int planes, int H, int cols) { return static_cast<size_t>(L) * 2 * planes * H * cols; }
 
 // The scale as a float; byte 0 (2^-127, no normal number) counts as 1.
 __device__ inline float mx_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(max(byte, 1)) << 23); }

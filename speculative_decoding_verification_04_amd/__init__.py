@@ -633,7 +633,8 @@ def spec_norm_rope_kv_mx_paged(q, k, v, codes, scales, layer: int, block_table, 
 
 
 def _unpack(name, paged, codes, scales, layer, where, kv_len, k_out, v_out, cu_seqlens, status, stream):
-    (L, planes, H, cols, D, _), dev, s, cache = _cache_at(codes, scales, codes.shape[3], stream)
+    heads = codes.shape[3] if codes.dim() == 6 else 0       # other shapes are refused there
+    (L, planes, H, cols, D, _), dev, s, cache = _cache_at(codes, scales, heads, stream)
     i32 = torch.int32
     B = where.shape[0] if paged else planes
     T, left = divmod(k_out.numel(), H * D)

@@ -718,7 +718,8 @@ int spec_tree_attention_paged(const void *q, int64_t q_stride, const void *pool,
  *   D            a multiple of 64, at most SPEC_ATTN_MAX_D
  *   codes, scales  multiples of 16 bytes; they may not overlap each other
  *   work-items   trees with N * G of at most 64: 512 (D > 128: 256) for each KV head of
- *                a sequence, and as many for up to 256 pieces more of long caches
+ *                a sequence, and as many for up to 256 pieces more of long caches;
+ *                norms: 64 a token (256 up to 256 of them, 128 up to 2048)
  *   between batches, trees with N * G of at most 64: whether a sequence's rows are cut
  *                at all follows B, H and the capacity (C, or max_pages * page_size)
  *

@@ -72,8 +72,8 @@ inline long long rope_grid(int tokens, int B, const void *status, int waves) {
   return static_cast<long long>(tokens) + (status ? (static_cast<long long>(B) + waves - 1) / waves : 0);
 }
 
-// Host checks of a call, into a cache of dt's elements or of 4-bit numbers; fills P.
-// threads: one token's heads, in whole waves.
+// Host checks of a call, into a cache of dt's elements or of 4-bit numbers, but for its
+// launch; fills P.  threads: one token's heads, in whole waves.
 struct RopeShape {
   Pairs pairs;
   int threads;
@@ -103,8 +103,6 @@ inline int rope_params(RopeParams &P, RopeShape &shape, bool mx, const void *q, 
   // one token's heads, in whole waves
   const long long lanes = static_cast<long long>(H) * (G + 2) * P.lanes;
   const int threads = static_cast<int>(lanes < kMaxThreads ? round_up(lanes, kWave) : kMaxThreads);
-  const int waves = threads / kWave;
-  if (!launchable(rope_grid(T, B, status, waves), threads)) return SPEC_EINVAL;
   const long long qh = static_cast<long long>(Hq) * D, kh = static_cast<long long>(H) * D;
   if (D * elt % 16 || q_stride < qh || k_stride < kh || v_stride < kh) return SPEC_EINVAL;
   if (q_stride * elt % 16 || k_stride * elt % 16 || v_stride * elt % 16) return SPEC_EINVAL;

@@ -233,7 +233,9 @@ int norm_rope_call(const void *q, int64_t q_stride, const void *k, int64_t k_str
                               cols, D, layer, T, B, N, G, table, max_pages, paged, end_col, kv_len, cu, positions,
                               q_weight, k_weight, eps, inv_freq, rot, interleaved, q_out, status);
   if (err) return err;
-  const unsigned grid = static_cast<unsigned>(rope_grid(T, B, status, shape.threads / kWave));
+  const long long workgroups = rope_grid(T, B, status, shape.threads / kWave);
+  if (!launchable(workgroups, shape.threads)) return SPEC_EINVAL;
+  const unsigned grid = static_cast<unsigned>(workgroups);
   (void)hipGetLastError();
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return dt == SPEC_BF16 ? launch_rope<__bf16>(P, shape.pairs, grid, shape.threads, s)

@@ -374,19 +374,19 @@ void launch_few(const Params &P, const Plan &p, unsigned grid, hipStream_t s) {
 template <typename T, int DP, bool MX>
 void launch_tree(const Params &P, const Plan &p, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.slots);
-  if constexpr (MX) {
-    if (p.few) {
-      if constexpr (DP == 256) {
-        if (P.c.D == 192) return launch_few<T, 192>(P, p, grid, s);
-      }
-      return launch_few<T, DP>(P, p, grid, s);
+  if constexpr (MX) {                                     // what is not few has more than 64 rows
+    if (!p.few) return launch_rows<T, DP, 4, true>(P, grid, s);
+    if constexpr (DP == 256) {
+      if (P.c.D == 192) return launch_few<T, 192>(P, p, grid, s);
     }
+    launch_few<T, DP>(P, p, grid, s);
+  } else {
+    if (p.rw == 4) return launch_rows<T, DP, 4, false>(P, grid, s);
+    if constexpr (sizeof(T) * DP <= 512) {
+      if (p.rw == 2) return launch_rows<T, DP, 2, false>(P, grid, s);
+    }
+    if constexpr (sizeof(T) * DP <= 256) launch_rows<T, DP, 1, false>(P, grid, s);
   }
-  if (p.rw == 4) return launch_rows<T, DP, 4, MX>(P, grid, s);
-  if constexpr (sizeof(T) * DP <= 512) {
-    if (p.rw == 2) return launch_rows<T, DP, 2, MX>(P, grid, s);
-  }
-  if constexpr (sizeof(T) * DP <= 256) launch_rows<T, DP, 1, MX>(P, grid, s);
 }
 
 template <typename T, int DP, bool MX>

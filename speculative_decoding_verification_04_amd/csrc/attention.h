@@ -147,33 +147,33 @@ struct Done {
   bool mine;
 };
 
-  // Takes infinities and NaNs out of the lane's own chunks of a V tile; whether
-  // there were any.  An exponent of all ones carries into the bit above it.
-  template <typename T, int DP, int RW>
+// Takes infinities and NaNs out of the lane's own chunks of a V tile; whether
+// there were any.  An exponent of all ones carries into the bit above it.
+template <typename T, int DP, int RW>
 __device__ inline bool clean_share(char *buf) {
   using S = Shape<T, DP, RW>;
-    u32x4 *own = reinterpret_cast<u32x4 *>(buf + S::kTile) + threadIdx.x;
-    constexpr uint32_t kExp = S::kElt == 2 ? 0x7f807f80u : 0x7f800000u, kOne = S::kElt == 2 ? 0x00800080u : 0x00800000u;
-    constexpr uint32_t kTop = S::kElt == 2 ? 0x80008000u : 0x80000000u;
-    uint32_t seen = 0;
+  u32x4 *own = reinterpret_cast<u32x4 *>(buf + S::kTile) + threadIdx.x;
+  constexpr uint32_t kExp = S::kElt == 2 ? 0x7f807f80u : 0x7f800000u, kOne = S::kElt == 2 ? 0x00800080u : 0x00800000u;
+  constexpr uint32_t kTop = S::kElt == 2 ? 0x80008000u : 0x80000000u;
+  uint32_t seen = 0;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const u32x4 x = own[i * kThreads];
+  for (int i = 0; i < S::kLoads; ++i) {
+    const u32x4 x = own[i * kThreads];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) seen |= (x[j] & kExp) + kOne;
-    }
-    if (!(seen & kTop)) return false;
-    for (int i = 0; i < S::kLoads; ++i) {
-      u32x4 x = own[i * kThreads];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t odd = ((x[j] & kExp) + kOne) & kTop;   // the top bit of each value to clear
-        x[j] &= S::kElt == 2 ? ~((odd >> 15) * 0xffffu) : odd ? 0u : ~0u;
-      }
-      own[i * kThreads] = x;
-    }
-    return true;
+    for (int j = 0; j < 4; ++j) seen |= (x[j] & kExp) + kOne;
   }
+  if (!(seen & kTop)) return false;
+  for (int i = 0; i < S::kLoads; ++i) {
+    u32x4 x = own[i * kThreads];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t odd = ((x[j] & kExp) + kOne) & kTop;   // the top bit of each value to clear
+      x[j] &= S::kElt == 2 ? ~((odd >> 15) * 0xffffu) : odd ? 0u : ~0u;
+    }
+    own[i * kThreads] = x;
+  }
+  return true;
+}
 
 // Brings K and V tiles from the cache straight into LDS.  A wave's load writes
 // 64 consecutive 16-byte places, so a lane takes the chunk whose place its own

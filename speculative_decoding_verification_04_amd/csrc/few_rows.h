@@ -44,10 +44,12 @@ struct Few {
   static constexpr int kKW = kWaves / RW;                 // waves behind each other
   static constexpr int kParts = sizeof(T) == 2 ? 1 : 3;   // bf16 parts of a number
   static constexpr int kShares = D / 64;                  // 16-byte shares of a row that a lane takes
-  // blocks in registers before they are used: two where the registers hold them (one more
-  // than they hold, 4-node float32 trees over 32 sequences of 512 .. 4096 rows, heads of
-  // 256, takes 207 us instead of 161)
-  static constexpr int kAhead = QB == 1 && (D <= 192 || sizeof(T) == 2) ? 2 : 1;
+  // blocks in registers before they are used: two where the registers hold them.  Float32
+  // heads of 128, whose queries take three parts on two waves a SIMD, and of 256 have no
+  // room for a second: with it, chains of 5 (28 heads of 128 over 4) take 18.5 us and not
+  // 16.2, 4-node trees over 32 sequences of 512 .. 4096 rows (heads of 256) 207 and not 161.
+  // (With one, 40 registers of the first and 59 of the second still go to scratch.)
+  static constexpr int kAhead = QB == 1 && (sizeof(T) == 2 || D == 64 || D == 192) ? 2 : 1;
   static constexpr int kRow = (D <= 64 ? 64 : D <= 128 ? 128 : 256) * 2;   // bytes of a row of V in LDS
   static constexpr int kStage = 32 * kRow;                // V of one wave
   static constexpr int kJoin = 32 * D * 4;                // outputs of 32 rows of one wave

@@ -21,11 +21,13 @@
 // Bound by issue: of a block's 1.1 us a wave at two waves a SIMD (64 rows of bf16, heads of
 // 128) the matrix instructions take half, the conversions and exponentials the most of the
 // other half, and the two overlap in part.  A workgroup's start, its first loads and its
-// join cost 8 or 9 us more.  Measured, both types at the clock under load: 16-node trees over
+// join cost 8 or 9 us more.  Not all that a wave holds fits its registers: 19 .. 22 go to
+// scratch in the loop for two blocks of 32 rows of heads of 128, 40 for float32 heads of 128
+// and 59 of 256.  Measured, both types at the clock under load: 16-node trees over
 // 32 sequences of 512 .. 4096 rows, 32 heads over 8, 44 us (the longest sequences' walks;
 // all of 4096 rows 53); 4-node trees over 32 sequences of 4096 rows 33 us = 4.4 TB/s of
 // codes and scales; chains of 5 in float32, 8 sequences of 64 .. 2048 rows in pages, 28
-// heads over 4, 19 us and the join 4; one token over 1100 rows 11 us.
+// heads over 4, 17 us and the join 4; one token over 1100 rows 11 us.
 // Not kept: products of the codes themselves (the scaled instructions add their products
 // up to 2^-12 of the sum's size apart); the next block's conversions beside this one's
 // products (56 us where this took 51: registers); a wave's loads in the order of the rows'

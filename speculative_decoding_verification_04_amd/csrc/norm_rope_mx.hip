@@ -11,9 +11,11 @@
 // token's place and angles, a lane for each pair, and keeps for its elements what turns
 // and weighs them, the same for all query heads: a head then costs a product, a sum and
 // a scaling an element.  Values go from bf16 to codes in one instruction a pair.
-// Measured, heads of 128, 32 over 8: 20.9k tokens (450 MB in and out) 108 us = 4.2 TB/s,
-// vector instructions issuing in three quarters of the cycles; 512 tokens into pages 10.5 us;
-// one token 6 us, the latency of three dependent loads and the float64 angles.
+// Measured, heads of 128, 32 over 8: 20.9k tokens (450 MB in and out) 113 us = 4.0 TB/s,
+// vector instructions issuing in three quarters of the cycles, in float32 (881 MB) 187 us;
+// 512 tokens into pages 10.6 us (as bf16 rows 7.5: here each of a token's two waves finds the
+// place and computes the angles); one token 6 us, the latency of three dependent loads and
+// the float64 angles.
 #include "norm_rope.h"
 
 namespace specv {
@@ -321,7 +323,7 @@ __global__ __launch_bounds__(kMaxThreads, 4) void norm_rope_mx_kernel(RopeParams
 template <typename T, Pairs PAIRS>
 void launch_pairs(const RopeParams &P, int split, int groups, unsigned grid, hipStream_t s) {
   // What a call reads and writes beyond the Infinity Cache (256 MB) is not found again:
-  // 20.9k tokens of 32 + 16 heads of 128 (451 MB) take 115 us so and 123 without.
+  // 20.9k tokens of 32 + 16 heads of 128 (451 MB) take 119 us so and 125 without.
   const long long bytes = static_cast<long long>(P.T) * (2 * P.Hq + 2 * P.c.H) * P.c.D * sizeof(T);
   if (bytes > (256ll << 20))
     hipLaunchKernelGGL((norm_rope_mx_kernel<T, PAIRS, true>), dim3(grid), dim3(kMaxThreads), 0, s, P, split, groups);
@@ -351,8 +353,13 @@ int norm_rope_mx_call(const void *q, int64_t q_stride, const void *k, int64_t k_
                               cols, D, layer, T, B, N, G, table, max_pages, paged, end_col, kv_len, cu, positions,
                               q_weight, k_weight, eps, inv_freq, rot, interleaved, q_out, status);
   if (err) return err;
-  // few tokens leave waves to spare: 512 tokens take 11.1 us with four waves each, 10.8
-  // with two and 13 to 15 with one; one token is alone in any case
+  // Few tokens leave waves to spare.  bf16, 32 heads of 128 over 8, captured calls with one /
+  // two / four waves a token: 1 token 9.8 / 7.3 / 6.4 us; 256: 11.5 / 8.6 / 7.7; 512: 12.0 / 9.4
+  // / 9.5; 1024: 12.8 / 11.3 / 12.6; 2048: 16.5 / 17.8 / 21.3; 4096: 26.0 / 30.3 / 37.3.  Fewer
+  // heads leave less to share, which the rule does not look at (2 heads over 2: 256 tokens
+  // 7.0 / 6.7 / 6.8; 1024: 7.7 / 8.3 / 10.2; 2048: 9.4 / 10.9 / 15.7), and in float32 it is
+  // within 1 us of the best for 32 heads over 8 but for 256 tokens (19.7 / 18.0 / 20.5) and
+  // loses up to 8 us for 2 over 2 there (11.0 / 13.5 / 18.9).
   const int split = T <= 256 ? 4 : T <= 2048 ? 2 : 1, per = kWaves / split, groups = (T + per - 1) / per;
   const long long grid = rope_grid(groups, B, status, kWaves);
   if (!launchable(grid, kMaxThreads)) return SPEC_EINVAL;

@@ -17,7 +17,7 @@
 // of the others); 8 prompts of 256 .. 2048 tokens, 14 heads of 64 over pages: 50 us
 // = 560 TFLOP/s, since heads of 64 halve the products but not the softmax; 4
 // prompts of 23 .. 64 tokens in float32: 8 us, latency.
-// Over 4-bit numbers prompts of 12001 and 9.9k tokens take 1.91 ms = 1057 TFLOP/s and
+// Over 4-bit numbers prompts of 12001 and 10147 tokens take 1.91 ms = 1057 TFLOP/s and
 // the second case 49 us: a tile's conversion
 // serves 128 query rows, and its bytes were not what bound it.
 #pragma once

@@ -57,8 +57,9 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
   p.kt = p.rw == 4 ? (dt == SPEC_BF16 ? 64 : 32) : 128 / p.rw;
   // Over 4-bit numbers, what a wave does with few query rows is converting, so waves of
   // their own do better than tiles that all share: 4-node trees over 32 sequences of 512 ..
-  // 4096 rows, 8 KV heads of 256, take 92 us and with tiles 192, in float32 161 and 1266;
-  // more rows than 64 of them would convert each cache row more than once.
+  // 4096 rows, 8 KV heads of 256, take 92 us and with tiles 192, in float32 161 and 1266
+  // (the other way round for one token of bf16 over 1000 rows of heads of 256: 19.4 and
+  // 16.4); more rows than 64 of them would convert each cache row more than once.
   p.few = mx && R <= 64;
   if (p.few) {
     p.rw = R > 32 ? 2 : 1;
@@ -81,6 +82,14 @@ inline Plan plan_of(int B, int N, int H, int G, int D, long long max_rows, spec_
     // that fill the chip gain by a cut only if their lengths differ: sequences of 64 ..
     // 8192 rows take 81 us in one launch and 90 in two, one of 8192 rows beside 31 of 64
     // takes 73 and 32, so a quarter of the longest walk counts as what a cut may save.
+    // A turn's time is not in the rule.  One launch / two, us, captured calls, sequences of
+    // one length, 8 KV heads: bf16 heads of 128, one token of 1 sequence, 640 rows 8.1 / 10.7,
+    // 1280 11.1 / 10.9, 2560 17.0 / 11.8; 16 nodes of 8 sequences, 640 rows 13.9 / 19.3, 1280
+    // 19.4 / 21.5, 2560 29.3 / 22.5: the rule is on the faster side or near it (it takes 640
+    // and 1280 rows in one launch).  Longer turns would pay for a cut earlier: 16 nodes of 1
+    // sequence, bf16 heads of 128, 1280 rows 18.6 / 16.5, float32 640 rows 21.8 / 17.5; one
+    // token, float32 heads of 128, 1280 rows 18.9 / 13.2, heads of 256, 640 rows, bf16 18.4 /
+    // 15.3 and float32 28.1 / 18.7; all of these go in one launch.
     const bool bf = dt == SPEC_BF16;
     const long long turn = 32 * (p.threads / kWave) / (p.rw == 2 && !(bf && D <= 128) ? 2 : 1);   // cache rows
     const long long idle = p.target - p.groups > p.target / 4 ? p.target - p.groups : p.target / 4;

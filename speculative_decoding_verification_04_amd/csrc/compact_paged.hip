@@ -14,7 +14,7 @@
 // path and its pages in one round of loads with a lane per slot, leaves the slots'
 // offsets in LDS, and moves units of up to 16 bytes.
 // Measured: 32 trees of 63 nodes with 2 .. 24 kept, 28 layers of 4 heads of 128 in bf16
-// (45 MB read and written) 13.5 us = 3.3 TB/s, two dependent rounds of loads before the
+// (45 MB read and written) 12.6 us = 3.6 TB/s, two dependent rounds of loads before the
 // first row moves; one tree of 16 nodes, 32 layers of 8 heads, 3.6 us.
 #include <algorithm>
 
